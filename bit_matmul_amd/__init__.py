@@ -19,7 +19,9 @@ from ._lib import (LQ_MULTI_MAX, LQ_ENCODE_MAX_D, LQ_ENCODE_MAX_SMALL_D, LQ_ENCO
                    LQ_ALGO_MFMA_SMALL,
                    LQ_ALGO_VALU, LQ_BF16, LQ_F32, LQ_MAX_D, LQ_MAX_HB, LQ_WS_CONTROL_BYTES,
                    LQ_WS_ERROR_WORD, LQ_NOALLOC_SCRATCH_BYTES, LQ_ERR_DEVICE, LQ_MAX_L, LQError,
-                   LQLayer, LQPlanInfo)
+                   LQLayer, LQPlanInfo, LQInt8Layer, LQNormBlockArgs, LQ_ACT_NONE, LQ_ACT_SILU,
+                   LQ_ACT_GELU, LQ_ACT_SIGMOID, LQ_ACT_TANH, LQ_NORM_POST, LQ_NORM_PRE,
+                   LQ_NORM_GATE_FIRST, LQ_NORM_ONE_PLUS, LQ_ROW_MAX_K, LQ_INT8_MAX_K)
 
 __all__ = [
     "lq_version", "lq_packed_size", "lq_pack_signs", "lq_unpack_signs", "lq_hadamard_scale",
@@ -35,6 +37,11 @@ __all__ = [
     "LQ_WS_ERROR_WORD", "library_path", "lq_linear_noalloc", "LQ_NOALLOC_SCRATCH_BYTES",
     "lq_linear_plan", "lq_sign_gemm_plan", "lq_workspace_status", "lq_debug_fused_timeout",
     "LQ_ERR_DEVICE", "LQ_MAX_L", "LQPlanInfo",
+    "lq_quant_rows", "int8_layer_struct", "lq_int8_gemm_workspace_size", "lq_int8_gemm",
+    "lq_int8_linear_workspace_size", "lq_int8_linear", "lq_norm_block", "LQInt8Layer",
+    "LQNormBlockArgs", "LQ_ACT_NONE", "LQ_ACT_SILU", "LQ_ACT_GELU", "LQ_ACT_SIGMOID",
+    "LQ_ACT_TANH", "LQ_NORM_POST", "LQ_NORM_PRE", "LQ_NORM_GATE_FIRST", "LQ_NORM_ONE_PLUS",
+    "LQ_ROW_MAX_K", "LQ_INT8_MAX_K",
 ]
 
 _DTYPES = {torch.float32: LQ_F32, torch.bfloat16: LQ_BF16}
@@ -311,3 +318,141 @@ def lq_profile_events(starts, stops) -> None:
         raise ValueError("starts and stops must have the same length")
     arr = ctypes.c_void_p * max(n, 1)
     _check(_lib.LIB.lq_profile_events(arr(*starts), arr(*stops), n), "lq_profile_events")
+
+
+def _rows(t, name: str, B: int, width: int):
+    """(address, row stride in elements) of a 2-D GPU tensor whose rows are
+    dense: a slice of a wider tensor is taken as it is."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a GPU tensor of two dimensions")
+    if t.size(0) < B or t.size(1) < width:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {B} rows of {width} are needed")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be dense")
+    # (a single row's stride says nothing)
+    return t.data_ptr(), t.stride(0) if t.size(0) > 1 else max(t.stride(0), width)
+
+
+def _rows8(t, name: str, B: int, K: int):
+    """_rows of 8-bit rows; each of them, the last too, owns its K rounded up
+    to 16 bytes."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int8:
+        raise ValueError(f"{name} must be an int8 tensor")
+    ptr, ld = _rows(t, name, B, K)
+    padded = -(-K // 16) * 16
+    if t.size(0) == 1:
+        ld = max(padded, -(-ld // 16) * 16)
+    end = t.storage_offset() + (B - 1) * ld + padded
+    if B > 0 and end > t.untyped_storage().nbytes():
+        raise ValueError(f"{name}'s last row must be padded to a multiple of 16 bytes")
+    return ptr, ld
+
+
+def _vec(t, name: str, n: int):
+    """The address of n dense floats; None stays None."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() < n:
+        raise ValueError(f"{name} must be {n} float32 values")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return _dev(t, name)
+
+
+def lq_quant_rows(x, B, K, q, scale, gate=None, act=LQ_ACT_NONE, hb=1, c=None, stream=None) -> None:
+    """8-bit rows q (int8, rows padded to 16 bytes) and scale (float32) of
+    T (act(gate) * x); x and gate: 2-D, of one dtype."""
+    xt = _dtype(x, "x")
+    xp, ldx = _rows(x, "x", B, K)
+    gp, ldg = None, 0
+    if gate is not None:
+        if gate.dtype != x.dtype:
+            raise ValueError("gate must have x's dtype")
+        gp, ldg = _rows(gate, "gate", B, K)
+    qp, ldq = _rows8(q, "q", B, K)
+    _check(_lib.LIB.lq_quant_rows(xp, xt, ldx, gp, ldg, act, B, K, hb, _vec(c, "c", K), qp, ldq,
+                                  _vec(scale, "scale", B), _stream(stream)), "lq_quant_rows")
+
+
+def int8_layer_struct(N, K, w, row_scale, hb=1, c=None, bias=None) -> LQInt8Layer:
+    """Fill a ``struct lq_int8_layer`` from device tensors (the caller keeps
+    the tensors alive while the struct is used); w: int8, N rows of K, each
+    padded to a multiple of 16 bytes."""
+    wp, ldw = _rows8(w, "w", N, K)
+    return LQInt8Layer(N, K, ldw, hb, 0, wp, _vec(c, "c", K), _vec(row_scale, "row_scale", N),
+                       _vec(bias, "bias", N))
+
+
+def lq_int8_gemm_workspace_size(layer: LQInt8Layer, B) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.LIB.lq_int8_gemm_workspace_size(ctypes.byref(layer), B, ctypes.byref(out)),
+           "lq_int8_gemm_workspace_size")
+    return out.value
+
+
+def lq_int8_gemm(layer: LQInt8Layer, q, scale, B, y, ws=None, stream=None) -> None:
+    """y = scale * row_scale * (q w^T) + bias for 8-bit rows q."""
+    qp, ldq = _rows8(q, "q", B, layer.K)
+    yp, ldy = _rows(y, "y", B, layer.N)
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(_lib.LIB.lq_int8_gemm(ctypes.byref(layer), qp, ldq, _vec(scale, "scale", B), B, yp,
+                                 _dtype(y, "y"), ldy, _opt(ws, "ws"), ws_bytes, _stream(stream)),
+           "lq_int8_gemm")
+
+
+def lq_int8_linear_workspace_size(layer: LQInt8Layer, B, xtype) -> int:
+    out = ctypes.c_size_t()
+    xt = _DTYPES[xtype] if isinstance(xtype, torch.dtype) else int(xtype)
+    _check(_lib.LIB.lq_int8_linear_workspace_size(ctypes.byref(layer), B, xt, ctypes.byref(out)),
+           "lq_int8_linear_workspace_size")
+    return out.value
+
+
+def lq_int8_linear(layer: LQInt8Layer, x, B, y, ws=None, stream=None) -> None:
+    """The whole 8-bit layer: x to 8-bit rows, then the product."""
+    xp, ldx = _rows(x, "x", B, layer.K)
+    yp, ldy = _rows(y, "y", B, layer.N)
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(_lib.LIB.lq_int8_linear(ctypes.byref(layer), xp, _dtype(x, "x"), ldx, B, yp,
+                                   _dtype(y, "y"), ldy, _opt(ws, "ws"), ws_bytes, _stream(stream)),
+           "lq_int8_linear")
+
+
+def lq_norm_block(B, K, y=None, gate=None, act=LQ_ACT_NONE, gate_first=False, post=False,
+                  w_post=None, h=None, alpha=1.0, h_out=None, pre=False, w_pre=None,
+                  one_plus=False, eps=1e-5, a=None, q=None, scale=None, stream=None) -> None:
+    """The norms after and before a block with its gate and scaled residual
+    (lq.h gives the formulas). gate: rows as y, or one vector of K for all."""
+    p = LQNormBlockArgs(B=B, K=K, act=act, alpha=alpha, eps=eps)
+    if y is not None:
+        p.ytype = _dtype(y, "y")
+        p.y, p.ldy = _rows(y, "y", B, K)
+    if gate is not None:
+        if y is None or gate.dtype != y.dtype:
+            raise ValueError("gate must have y's dtype")
+        if gate.dim() == 1:
+            if gate.numel() < K or gate.device.index != torch.cuda.current_device():
+                raise ValueError(f"gate must hold {K} values on the current device")
+            p.gate, p.ldg = _dev(gate, "gate"), 0
+        else:
+            p.gate, p.ldg = _rows(gate, "gate", B, K)
+    if h is not None:
+        p.htype = _dtype(h, "h")
+        p.h, p.ldh = _rows(h, "h", B, K)
+    if h_out is not None:
+        if h is not None and h_out.dtype != h.dtype:
+            raise ValueError("h_out must have h's dtype")
+        p.htype = _dtype(h_out, "h_out")
+        p.h_out, p.ldh_out = _rows(h_out, "h_out", B, K)
+    if a is not None:
+        p.atype = _dtype(a, "a")
+        p.a, p.lda = _rows(a, "a", B, K)
+    if q is not None:
+        p.q, p.ldq = _rows8(q, "q", B, K)
+    p.scale = _vec(scale, "scale", B)
+    p.w_post, p.w_pre = _vec(w_post, "w_post", K), _vec(w_pre, "w_pre", K)
+    p.flags = ((LQ_NORM_POST if post else 0) | (LQ_NORM_PRE if pre else 0) |
+               (LQ_NORM_GATE_FIRST if gate_first else 0) | (LQ_NORM_ONE_PLUS if one_plus else 0))
+    _check(_lib.LIB.lq_norm_block(ctypes.byref(p), _stream(stream)), "lq_norm_block")

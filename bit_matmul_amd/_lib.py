@@ -2,7 +2,7 @@
 from __future__ import annotations
 
 import ctypes
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().parent / "liblq.so"
@@ -21,6 +21,10 @@ LQ_ENCODE_MAX_SMALL_D = 16
 LQ_ENCODE_PINV_MAX_D = 32
 LQ_ENCODE_PINV_MAX_FREE = 24
 LQ_MULTI_MAX = 4
+LQ_ACT_NONE, LQ_ACT_SILU, LQ_ACT_GELU, LQ_ACT_SIGMOID, LQ_ACT_TANH = range(5)
+LQ_NORM_POST, LQ_NORM_PRE, LQ_NORM_GATE_FIRST, LQ_NORM_ONE_PLUS = 1, 2, 4, 8
+LQ_ROW_MAX_K = 65536
+LQ_INT8_MAX_K = 131071
 LQ_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 # Every symbol include/lq.h declares.
@@ -33,7 +37,8 @@ EXPORTS = [
     "lq_train_m_step_workspace_size", "lq_train_m_step", "lq_linear_multi_workspace_size",
     "lq_linear_multi", "lq_linear_noalloc", "lq_linear_plan", "lq_sign_gemm_plan",
     "lq_workspace_status", "lq_debug_fused_timeout", "lq_encode_pinv_workspace_size",
-    "lq_encode_pinv",
+    "lq_encode_pinv", "lq_quant_rows", "lq_int8_gemm_workspace_size", "lq_int8_gemm",
+    "lq_int8_linear_workspace_size", "lq_int8_linear", "lq_norm_block",
 ]
 
 
@@ -51,6 +56,28 @@ class LQPlanInfo(ctypes.Structure):
     _fields_ = [
         ("algo", c_int32), ("workgroups", c_int32), ("waves", c_int32), ("panels", c_int32),
         ("batch_rows", c_int32), ("ksplit", c_int32),
+    ]
+
+
+class LQInt8Layer(ctypes.Structure):
+    """Mirror of ``struct lq_int8_layer``."""
+    _fields_ = [
+        ("N", c_int64), ("K", c_int64), ("ldw", c_int64), ("hb", c_int32), ("reserved", c_int32),
+        ("w", c_void_p), ("c", c_void_p), ("row_scale", c_void_p), ("bias", c_void_p),
+    ]
+
+
+class LQNormBlockArgs(ctypes.Structure):
+    """Mirror of ``struct lq_norm_block_args``."""
+    _fields_ = [
+        ("B", c_int64), ("K", c_int64),
+        ("y", c_void_p), ("gate", c_void_p), ("w_post", c_void_p), ("h", c_void_p),
+        ("h_out", c_void_p), ("w_pre", c_void_p), ("a", c_void_p), ("q", c_void_p),
+        ("scale", c_void_p),
+        ("ldy", c_int64), ("ldg", c_int64), ("ldh", c_int64), ("ldh_out", c_int64),
+        ("lda", c_int64), ("ldq", c_int64),
+        ("ytype", c_int32), ("htype", c_int32), ("atype", c_int32), ("act", c_int32),
+        ("alpha", c_float), ("eps", c_float), ("flags", c_uint32), ("reserved", c_uint32),
     ]
 
 
@@ -103,6 +130,15 @@ def _load():
         "lq_workspace_status": (c_int, [vp, sz, vp]),
         "lq_debug_fused_timeout": (c_int, [i32]),
         "lq_profile_events": (c_int, [POINTER(vp), POINTER(vp), i32]),
+        "lq_quant_rows": (c_int, [vp, c_int, i64, vp, i64, c_int, i64, i64, i32, vp, vp, i64, vp,
+                                  vp]),
+        "lq_int8_gemm_workspace_size": (c_int, [POINTER(LQInt8Layer), i64, POINTER(sz)]),
+        "lq_int8_gemm": (c_int, [POINTER(LQInt8Layer), vp, i64, vp, i64, vp, c_int, i64, vp, sz,
+                                 vp]),
+        "lq_int8_linear_workspace_size": (c_int, [POINTER(LQInt8Layer), i64, c_int, POINTER(sz)]),
+        "lq_int8_linear": (c_int, [POINTER(LQInt8Layer), vp, c_int, i64, i64, vp, c_int, i64, vp,
+                                   sz, vp]),
+        "lq_norm_block": (c_int, [POINTER(LQNormBlockArgs), vp]),
     }
     for name, (res, args) in protos.items():
         fn = getattr(lib, name)

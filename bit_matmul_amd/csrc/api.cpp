@@ -98,6 +98,7 @@ hipError_t profiled(hipStream_t stream, Fn fn) {
 static_assert(lq::kControlBytes == LQ_WS_CONTROL_BYTES, "control area size");
 static_assert(lq::kFusedErrorWord == LQ_WS_ERROR_WORD, "error word");
 static_assert(lq::kMultiMax == LQ_MULTI_MAX, "layers per grouped call");
+static_assert((size_t)LQ_INT8_MAX_K * 128 * 128 <= INT32_MAX, "a sum of byte products fits 32 bits");
 
 // Compute units of the current device (0 when there is none), cached.
 int device_cus() {
@@ -964,6 +965,202 @@ lq_status lq_profile_events(void* const* starts, void* const* stops, int32_t cou
     ring.stops.push_back(static_cast<hipEvent_t>(stops[i]));
   }
   return LQ_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- 8-bit layers and norms
+
+namespace {
+
+bool valid_act(int32_t act) { return act >= LQ_ACT_NONE && act <= LQ_ACT_TANH; }
+bool aligned_to(const void* p, lq_dtype t) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (t == LQ_F32 ? 3u : 1u)) == 0;
+}
+int64_t round16(int64_t v) { return (v + 15) & ~int64_t(15); }
+
+lq_status check_rows(int64_t B, int64_t K, int64_t max_k) {
+  if (B < 0 || K < 1) return LQ_ERR_INVALID_ARG;
+  if (B > kMaxBatch || K > max_k) return LQ_ERR_UNSUPPORTED;
+  return LQ_OK;
+}
+// Rows `ld` apart that hold `width` elements each.
+lq_status check_ld(int64_t ld, int64_t width) {
+  if (ld < width) return LQ_ERR_INVALID_ARG;
+  return ld > kMaxDim * int64_t(16) ? LQ_ERR_UNSUPPORTED : LQ_OK;
+}
+lq_status check_q(const int8_t* q, int64_t ldq, int64_t K) {
+  if (!aligned16(q) || ldq % 16 != 0) return LQ_ERR_INVALID_ARG;
+  return check_ld(ldq, round16(K));
+}
+lq_status check_hb(int64_t K, int32_t hb) {
+  if (hb < 1 || !is_pow2(hb)) return LQ_ERR_INVALID_ARG;
+  if (hb > LQ_MAX_HB) return LQ_ERR_UNSUPPORTED;
+  return K % hb == 0 ? LQ_OK : LQ_ERR_INVALID_ARG;
+}
+
+lq_status check_int8_layer(const lq_int8_layer* l, int64_t B, int64_t max_k) {
+  if (l == nullptr || l->reserved != 0 || l->N < 0) return LQ_ERR_INVALID_ARG;
+  if (l->N > kMaxDim) return LQ_ERR_UNSUPPORTED;
+  lq_status s = check_rows(B, l->K, max_k);
+  if (s == LQ_OK) s = check_hb(l->K, l->hb);
+  if (s == LQ_OK && l->ldw % 16 != 0) s = LQ_ERR_INVALID_ARG;
+  if (s == LQ_OK) s = check_ld(l->ldw, round16(l->K));
+  if (s == LQ_OK && !mul_ok(B, l->N, kMaxElems)) s = LQ_ERR_UNSUPPORTED;
+  return s;
+}
+
+// The pieces of lq_int8_linear's workspace, behind the control area.
+struct Int8Ws {
+  size_t off_q, off_scale, off_gemm, total;
+  int64_t ldq;
+};
+Int8Ws int8_ws(const lq_int8_layer* l, int64_t B) {
+  Int8Ws w;
+  w.ldq = round16(l->K);
+  w.off_q = align_up(lq::kControlBytes);
+  w.off_scale = w.off_q + align_up((size_t)B * w.ldq);
+  w.off_gemm = w.off_scale + align_up((size_t)B * sizeof(float));
+  w.total = w.off_gemm;
+  return w;
+}
+
+void fill_hb(lq::QuantRows* p, int32_t hb) {
+  p->lhb = 0;
+  while ((1 << p->lhb) < hb) ++p->lhb;
+  // 1/sqrt(hb) for hb = 2^k: exact when k is even, correctly rounded otherwise.
+  p->norm = p->lhb % 2 == 0 ? ldexpf(1.0f, -p->lhb / 2) : (float)(1.0 / sqrt((double)hb));
+}
+
+lq_status check_gemm_ptrs(const lq_int8_layer* l, const void* y, lq_dtype ytype, int64_t ldy) {
+  if (!valid_dtype(ytype) || !aligned_to(y, ytype)) return LQ_ERR_INVALID_ARG;
+  if (!aligned16(l->w) || !aligned_to(l->row_scale, LQ_F32)) return LQ_ERR_INVALID_ARG;
+  if (l->bias != nullptr && !aligned_to(l->bias, LQ_F32)) return LQ_ERR_INVALID_ARG;
+  return check_ld(ldy, l->N);
+}
+
+lq::Int8Gemm gemm_args(const lq_int8_layer* l, const int8_t* q, int64_t ldq, const float* scale,
+                       int64_t B, void* y, lq_dtype ytype, int64_t ldy) {
+  return {q, scale, l->w, l->row_scale, l->bias, y, B, l->N, l->K, ldq, l->ldw, ldy,
+          ytype == LQ_BF16};
+}
+
+}  // namespace
+
+extern "C" {
+
+lq_status lq_quant_rows(const void* x, lq_dtype xtype, int64_t ldx, const void* gate, int64_t ldg,
+                        lq_act act, int64_t B, int64_t K, int32_t hb, const float* c, int8_t* q,
+                        int64_t ldq, float* scale, void* stream) {
+  if (!valid_dtype(xtype) || !valid_act(act)) return LQ_ERR_INVALID_ARG;
+  lq_status s = check_rows(B, K, LQ_ROW_MAX_K);
+  if (s == LQ_OK) s = check_hb(K, hb);
+  if (s == LQ_OK) s = check_ld(ldx, K);
+  if (s == LQ_OK && gate != nullptr) s = check_ld(ldg, K);
+  if (s != LQ_OK) return s;
+  if (B == 0) return LQ_OK;
+  if (!aligned_to(x, xtype) || (gate != nullptr && !aligned_to(gate, xtype))) return LQ_ERR_INVALID_ARG;
+  if ((c != nullptr && !aligned_to(c, LQ_F32)) || !aligned_to(scale, LQ_F32)) return LQ_ERR_INVALID_ARG;
+  s = check_q(q, ldq, K);
+  if (s != LQ_OK) return s;
+  lq::QuantRows p{x, gate, c, q, scale, B, K, ldx, ldg, ldq, (int)act, 0, 1.0f, xtype == LQ_BF16};
+  fill_hb(&p, hb);
+  return hip_status(lq::launch_quant_rows(p, (hipStream_t)stream));
+}
+
+lq_status lq_int8_gemm_workspace_size(const lq_int8_layer* layer, int64_t B, size_t* bytes) {
+  if (bytes == nullptr) return LQ_ERR_INVALID_ARG;
+  lq_status s = check_int8_layer(layer, B, LQ_INT8_MAX_K);
+  if (s != LQ_OK) return s;
+  *bytes = 0;
+  return LQ_OK;
+}
+
+lq_status lq_int8_gemm(const lq_int8_layer* layer, const int8_t* q, int64_t ldq,
+                       const float* scale, int64_t B, void* y, lq_dtype ytype, int64_t ldy,
+                       void* ws, size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  lq_status s = lq_int8_gemm_workspace_size(layer, B, &need);
+  if (s != LQ_OK) return s;
+  if (B == 0 || layer->N == 0) return LQ_OK;
+  s = check_gemm_ptrs(layer, y, ytype, ldy);
+  if (s == LQ_OK && !aligned_to(scale, LQ_F32)) s = LQ_ERR_INVALID_ARG;
+  if (s == LQ_OK) s = check_q(q, ldq, layer->K);
+  if (s == LQ_OK) s = check_ws(ws, ws_bytes, need);
+  if (s != LQ_OK) return s;
+  return hip_status(lq::launch_int8_gemm(gemm_args(layer, q, ldq, scale, B, y, ytype, ldy),
+                                         (hipStream_t)stream));
+}
+
+lq_status lq_int8_linear_workspace_size(const lq_int8_layer* layer, int64_t B, lq_dtype xtype,
+                                        size_t* bytes) {
+  if (bytes == nullptr || !valid_dtype(xtype)) return LQ_ERR_INVALID_ARG;
+  lq_status s = check_int8_layer(layer, B, LQ_ROW_MAX_K);
+  if (s != LQ_OK) return s;
+  *bytes = B == 0 || layer->N == 0 ? 0 : int8_ws(layer, B).total;
+  return LQ_OK;
+}
+
+lq_status lq_int8_linear(const lq_int8_layer* layer, const void* x, lq_dtype xtype, int64_t ldx,
+                         int64_t B, void* y, lq_dtype ytype, int64_t ldy, void* ws,
+                         size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  lq_status s = lq_int8_linear_workspace_size(layer, B, xtype, &need);
+  if (s != LQ_OK) return s;
+  if (B == 0 || layer->N == 0) return LQ_OK;
+  s = check_ld(ldx, layer->K);
+  if (s == LQ_OK && !aligned_to(x, xtype)) s = LQ_ERR_INVALID_ARG;
+  if (s == LQ_OK && layer->c != nullptr && !aligned_to(layer->c, LQ_F32)) s = LQ_ERR_INVALID_ARG;
+  if (s == LQ_OK) s = check_gemm_ptrs(layer, y, ytype, ldy);
+  if (s == LQ_OK) s = check_ws(ws, ws_bytes, need);
+  if (s != LQ_OK) return s;
+  const Int8Ws w = int8_ws(layer, B);
+  char* base = static_cast<char*>(ws);
+  int8_t* q = reinterpret_cast<int8_t*>(base + w.off_q);
+  float* scale = reinterpret_cast<float*>(base + w.off_scale);
+  lq::QuantRows p{x, nullptr, layer->c, q, scale, B, layer->K, ldx, 0, w.ldq, LQ_ACT_NONE, 0, 1.0f,
+                  xtype == LQ_BF16};
+  fill_hb(&p, layer->hb);
+  s = hip_status(lq::launch_quant_rows(p, (hipStream_t)stream));
+  if (s != LQ_OK) return s;
+  return hip_status(lq::launch_int8_gemm(gemm_args(layer, q, w.ldq, scale, B, y, ytype, ldy),
+                                         (hipStream_t)stream));
+}
+
+lq_status lq_norm_block(const lq_norm_block_args* a, void* stream) {
+  if (a == nullptr || a->reserved != 0) return LQ_ERR_INVALID_ARG;
+  constexpr uint32_t kFlags = LQ_NORM_POST | LQ_NORM_PRE | LQ_NORM_GATE_FIRST | LQ_NORM_ONE_PLUS;
+  if ((a->flags & ~kFlags) != 0 || !valid_act(a->act)) return LQ_ERR_INVALID_ARG;
+  const bool post = a->flags & LQ_NORM_POST, pre = a->flags & LQ_NORM_PRE;
+  const lq_dtype yt = (lq_dtype)a->ytype, ht = (lq_dtype)a->htype, at = (lq_dtype)a->atype;
+  if ((post || pre) && !(a->eps > 0.0f && std::isfinite(a->eps))) return LQ_ERR_INVALID_ARG;
+  if (!std::isfinite(a->alpha)) return LQ_ERR_INVALID_ARG;
+  if (a->y == nullptr && (a->gate != nullptr || post)) return LQ_ERR_INVALID_ARG;
+  if ((a->q == nullptr) != (a->scale == nullptr)) return LQ_ERR_INVALID_ARG;
+  if ((a->y != nullptr && !valid_dtype(yt)) || (a->a != nullptr && !valid_dtype(at)) ||
+      ((a->h != nullptr || a->h_out != nullptr) && !valid_dtype(ht)))
+    return LQ_ERR_INVALID_ARG;
+  lq_status s = check_rows(a->B, a->K, LQ_ROW_MAX_K);
+  if (s == LQ_OK && a->y != nullptr) s = check_ld(a->ldy, a->K);
+  if (s == LQ_OK && a->gate != nullptr && a->ldg != 0) s = check_ld(a->ldg, a->K);
+  if (s == LQ_OK && a->h != nullptr) s = check_ld(a->ldh, a->K);
+  if (s == LQ_OK && a->h_out != nullptr) s = check_ld(a->ldh_out, a->K);
+  if (s == LQ_OK && a->a != nullptr) s = check_ld(a->lda, a->K);
+  if (s == LQ_OK && a->q != nullptr) s = check_q(a->q, a->ldq, a->K);
+  if (s != LQ_OK) return s;
+  if (a->B == 0) return LQ_OK;
+  if (a->y == nullptr && a->h == nullptr) return LQ_ERR_INVALID_ARG;
+  if (a->h_out == nullptr && a->a == nullptr && a->q == nullptr) return LQ_ERR_INVALID_ARG;
+  auto ok = [](const void* p, lq_dtype t) { return p == nullptr || aligned_to(p, t); };
+  if (!ok(a->y, yt) || !ok(a->gate, yt) || !ok(a->h, ht) || !ok(a->h_out, ht) || !ok(a->a, at) ||
+      !ok(a->w_post, LQ_F32) || !ok(a->w_pre, LQ_F32) || !ok(a->scale, LQ_F32))
+    return LQ_ERR_INVALID_ARG;
+  const lq::NormBlock p{a->y, a->gate, a->w_post, a->h, a->h_out, a->w_pre, a->a, a->q, a->scale,
+                        a->B, a->K, a->ldy, a->ldg, a->ldh, a->ldh_out, a->lda, a->ldq,
+                        a->alpha, a->eps, a->act, yt == LQ_BF16, ht == LQ_BF16, at == LQ_BF16,
+                        post, pre, (a->flags & LQ_NORM_GATE_FIRST) != 0,
+                        (a->flags & LQ_NORM_ONE_PLUS) != 0};
+  return hip_status(lq::launch_norm_block(p, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -371,6 +371,140 @@ lq_status lq_linear_multi(const lq_layer* layers, int32_t n, const void* x, lq_d
                           void* stream);
 
 /*
+ * 8-bit layers: the layers of a model that are kept at 8 bits next to the
+ * lifted ones ([review] Limitations: the lifted code is weak near 4 bits and
+ * above; paper §1: the memory left over depends on the output head's
+ * precision). Symmetric, one scale for each token and one for each output:
+ *
+ *     v    = T (act(gate) .* x)            (act(gate) and T optional)
+ *     s    = max_k |v_k| / 127
+ *     q_k  = v_k * 127 / max|v|, rounded to the nearest whole number, ties
+ *            to even (a row of zeros: s = 0, q = 0; a row holding an
+ *            infinity or a NaN: s = NaN, q = 0, so its outputs are NaN)
+ *     y[n] = s * row_scale[n] * sum_k w[n][k] q[k]  (+ bias[n])
+ *
+ * T is the lifted layer's (hb, c); the weights of such a layer are
+ * W T^-1, as a lifted layer's. The sum over k is exact.
+ *
+ * Rows of these entry points may lie `ld` elements apart (ld >= K or N): a
+ * slice of a wider product is taken as it is. Rows of x, gate, y and h need
+ * only their element's alignment. 8-bit rows are padded to a multiple of 16
+ * bytes: their ld is a multiple of 16, their first row is 16-byte aligned, every row
+ * (the last too) owns its K rounded up to 16 bytes, and of q's rows the bytes
+ * from K to there are zero (every entry point that writes q writes them so);
+ * of w's rows those bytes may hold anything.
+ */
+typedef enum lq_act {
+  LQ_ACT_NONE = 0,
+  LQ_ACT_SILU = 1,          /* g / (1 + exp(-g)) */
+  LQ_ACT_GELU = 2,          /* g / 2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+  LQ_ACT_SIGMOID = 3,
+  LQ_ACT_TANH = 4
+} lq_act;
+
+#define LQ_ROW_MAX_K 65536    /* longest row of lq_quant_rows and lq_norm_block */
+#define LQ_INT8_MAX_K 131071  /* longest sum of products of bytes that 32 bits hold */
+
+/* One 8-bit linear layer (all pointers device, caller-owned). Layers that
+ * read the same input are one layer of more rows. */
+typedef struct lq_int8_layer {
+  int64_t N;                 /* output features */
+  int64_t K;                 /* input features */
+  int64_t ldw;               /* bytes from one row of w to the next, a multiple of 16 */
+  int32_t hb;                /* Hadamard block of T, as in lq_layer; 1: none */
+  int32_t reserved;          /* must be 0 */
+  const int8_t* w;           /* N rows of K weights */
+  const float* c;            /* K channel scales of T; NULL: none (all one) */
+  const float* row_scale;    /* N scales */
+  const float* bias;         /* N values, or NULL */
+} lq_int8_layer;
+
+/*
+ * 8-bit rows q, scale of act(gate) .* x (formulas above). x: B rows of K in
+ * xtype, ldx elements apart; gate: NULL, or rows of the same type ldg apart;
+ * c: K channel scales or NULL, hb: as in lq_hadamard_scale; q: B rows, ldq
+ * apart; scale: B floats. v is computed in fp32; the rounding to 8 bits is
+ * that of the exact quotient. Errors: INVALID_ARG for a NULL or misaligned pointer, a
+ * negative size, K < 1, ld below K, ldq not a multiple of 16, an unknown act
+ * or dtype, hb not a power of two or not a divisor of K; UNSUPPORTED for
+ * K > LQ_ROW_MAX_K or hb > LQ_MAX_HB.
+ */
+lq_status lq_quant_rows(const void* x, lq_dtype xtype, int64_t ldx, const void* gate, int64_t ldg,
+                        lq_act act, int64_t B, int64_t K, int32_t hb, const float* c, int8_t* q,
+                        int64_t ldq, float* scale, void* stream);
+
+/*
+ * The product of 8-bit rows (lq_quant_rows', lq_norm_block's) with the
+ * layer's weights: y, B rows of N in ytype, ldy elements apart. The layer's
+ * hb and c are not used. y = (float)sum * (scale * row_scale) + bias in fp32,
+ * rounded once to ytype. ws: device workspace of at least
+ * lq_int8_gemm_workspace_size bytes (may be NULL when that size is 0).
+ * Errors: INVALID_ARG as above; UNSUPPORTED for K > LQ_INT8_MAX_K;
+ * WORKSPACE for a missing or short workspace.
+ */
+lq_status lq_int8_gemm_workspace_size(const lq_int8_layer* layer, int64_t B, size_t* bytes);
+lq_status lq_int8_gemm(const lq_int8_layer* layer, const int8_t* q, int64_t ldq,
+                       const float* scale, int64_t B, void* y, lq_dtype ytype, int64_t ldy,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The whole 8-bit layer: lq_quant_rows of x with the layer's T, then
+ * lq_int8_gemm, the 8-bit rows in the workspace (behind its control area,
+ * which is left as it is). Errors: as those two.
+ */
+lq_status lq_int8_linear_workspace_size(const lq_int8_layer* layer, int64_t B, lq_dtype xtype,
+                                        size_t* bytes);
+lq_status lq_int8_linear(const lq_int8_layer* layer, const void* x, lq_dtype xtype, int64_t ldx,
+                         int64_t B, void* y, lq_dtype ytype, int64_t ldy, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/*
+ * The norms before and after a block of a model, with the block's gate and
+ * scaled residual, in one pass over the row:
+ *
+ *     u  = y                                  (the block's output)
+ *     u  = act(gate) .* u                     with LQ_NORM_GATE_FIRST
+ *     u  = u / sqrt(mean(u^2) + eps) .* w     with LQ_NORM_POST, w = w_post
+ *     u  = act(gate) .* u                     without LQ_NORM_GATE_FIRST
+ *     h' = h + alpha u                        written to h_out
+ *     a  = h' / sqrt(mean(h'^2) + eps) .* w   with LQ_NORM_PRE, w = w_pre
+ *                                             (else a = h')
+ *
+ * a is written as values (a) or as 8-bit rows (q, scale), or both. fp32
+ * throughout; the second norm reads h' before it is rounded to htype.
+ * NULL gate: no gate. NULL w: all ones. LQ_NORM_ONE_PLUS: 1 + w in place of
+ * w. NULL y: h' = h. NULL h: h' = alpha u. NULL h_out, a, q: not written (one
+ * is needed); q and scale go together. ldg == 0: one gate for every row.
+ * h_out may be h, and a may be y or h, with the same type and ld; nothing
+ * else may overlap. Errors: INVALID_ARG as above, for both y and h NULL, a gate or
+ * LQ_NORM_POST without y, h_out without htype, eps not positive and finite
+ * with a norm, alpha not finite, unknown flags; UNSUPPORTED for K > LQ_ROW_MAX_K.
+ */
+#define LQ_NORM_POST 1u
+#define LQ_NORM_PRE 2u
+#define LQ_NORM_GATE_FIRST 4u
+#define LQ_NORM_ONE_PLUS 8u
+typedef struct lq_norm_block_args {
+  int64_t B, K;
+  const void* y;             /* ytype, ldy */
+  const void* gate;          /* ytype, ldg (0: one row for all) */
+  const float* w_post;
+  const void* h;             /* htype, ldh */
+  void* h_out;               /* htype, ldh_out */
+  const float* w_pre;
+  void* a;                   /* atype, lda */
+  int8_t* q;                 /* ldq, a multiple of 16 */
+  float* scale;
+  int64_t ldy, ldg, ldh, ldh_out, lda, ldq;
+  int32_t ytype, htype, atype;   /* lq_dtype */
+  int32_t act;                   /* lq_act */
+  float alpha, eps;
+  uint32_t flags;            /* LQ_NORM_* */
+  uint32_t reserved;         /* must be 0 */
+} lq_norm_block_args;
+lq_status lq_norm_block(const lq_norm_block_args* args, void* stream);
+
+/*
  * Prepare a workspace for first use: zero-fill its control area (the first
  * min(ws_bytes, LQ_WS_CONTROL_BYTES) bytes, with a kernel on `stream`).
  * Errors: INVALID_ARG for a NULL or unaligned ws with ws_bytes > 0.
