@@ -10,12 +10,10 @@
 // N and tokens past B are read as the last one and never stored. K is taken
 // up to the next multiple of 16 (the codes' pad is zero); the last 64-byte
 // step past that is read as zero codes.
-#include "lq_internal.h"
+#include "lq_int8.h"
 
 namespace lq {
 namespace {
-
-typedef __attribute__((ext_vector_type(4))) int i32x4;
 
 template <int P, int T>
 __global__ __launch_bounds__(512) void int8_stream_kernel(Int8Gemm p, int tiles_n) {
@@ -84,15 +82,11 @@ __global__ __launch_bounds__(512) void int8_stream_kernel(Int8Gemm p, int tiles_
     const int i = (t >> 6) / T, j = (t >> 6) % T;
     const int64_t n = n0 + 16 * i + 4 * ((t >> 4) & 3), b = b0 + 16 * j + (t & 15);
     if (b >= p.B) continue;
-    const float sb = p.scale[b];
+    if (n >= p.N) continue;
+    i32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (n + e >= p.N) break;
-      float v = (float)sum[((t >> 6) * 4 + e) * 64 + (t & 63)] * (sb * p.row_scale[n + e]);
-      if (p.bias != nullptr) v += p.bias[n + e];
-      if (p.y_bf16) reinterpret_cast<uint16_t*>(p.y)[b * p.ldy + n + e] = (uint16_t)f32_to_bf16_bits(v);
-      else reinterpret_cast<float*>(p.y)[b * p.ldy + n + e] = v;
-    }
+    for (int e = 0; e < 4; ++e) v[e] = sum[((t >> 6) * 4 + e) * 64 + (t & 63)];
+    store_int8_sums(p, b, n, p.scale[b], v);
   }
 }
 
@@ -101,6 +95,7 @@ __global__ __launch_bounds__(512) void int8_stream_kernel(Int8Gemm p, int tiles_
 hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t stream) {
   (void)hipGetLastError();   // clear a stale error of an earlier runtime call
   const int64_t tiles_n = (p.N + 15) / 16;
+  if (p.B > 64) return launch_int8_tile(p, stream);
   if (p.B <= 16) {
     hipLaunchKernelGGL((int8_stream_kernel<1, 1>), dim3((unsigned)tiles_n), dim3(512), 0, stream, p,
                        (int)tiles_n);

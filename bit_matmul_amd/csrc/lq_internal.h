@@ -518,5 +518,6 @@ RowShape row_shape(int64_t K);
 hipError_t launch_quant_rows(const QuantRows& p, hipStream_t stream);
 hipError_t launch_norm_block(const NormBlock& p, hipStream_t stream);
 hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t stream);
+hipError_t launch_int8_tile(const Int8Gemm& p, hipStream_t stream);
 
 }  // namespace lq
