@@ -27,15 +27,24 @@
 namespace lq {
 namespace {
 
-// 16 zero bytes for the chunks of q past K.
-__device__ const uint4 kZeroChunk = {0, 0, 0, 0};
+// acc += a c with acc held in accumulation registers: left to itself the
+// compiler spreads 256 sums over both register files and spills. The
+// operands were waited for before the step's barrier; the readers of acc
+// wait for the last products (acc_ready).
+__device__ __forceinline__ void mfma_acc(i32x4& acc, i32x4 a, i32x4 c) {
+  acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, c, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mfma_zero(i32x4& acc) {
+  acc = (i32x4){0, 0, 0, 0};
+  asm("" : "+a"(acc));
+}
+__device__ __forceinline__ void acc_ready() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 template <int PN, int PB>
 __global__ __launch_bounds__(256, 1) void int8_tile_kernel(Int8Gemm p, int tiles_n, int tiles_b,
                                                            int group_n) {
   constexpr int kBlocks = 2 * PN + 2 * PB;
-  constexpr int kCopies = kBlocks / 4;
-  constexpr int kStages = 4;
+  constexpr int kCopies = (kBlocks + 3) / 4;
   __shared__ uint4 stage0[kBlocks * 64];
   __shared__ uint4 stage1[kBlocks * 64];
   __shared__ uint4 stage2[kBlocks * 64];
@@ -51,65 +60,59 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(Int8Gemm p, int tiles
   const int tiles = tiles_n * tiles_b;
   const int per = (tiles + 7) / 8;
   const int t = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
-  if (((int)blockIdx.x >> 3) >= per || t >= tiles) return;
+  if (t >= tiles) return;
   const int gsize = group_n * tiles_b;
   const int grp = t / gsize, in = t % gsize;
   const int gn = min(group_n, tiles_n - grp * group_n);
-  const int64_t n0 = (int64_t)(grp * group_n + in % gn) * (32 * PN);
-  const int64_t b0 = (int64_t)(in / gn) * (32 * PB);
+  // (divisions leave the scalar unit: back to it, for scalar addresses)
+  const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(grp * group_n + in % gn) * (32 * PN);
+  const int64_t b0 = (int64_t)__builtin_amdgcn_readfirstlane(in / gn) * (32 * PB);
 
   const int K16 = ((int)p.K + 15) & ~15;
-  const int steps = (K16 + 63) / 64;
+  const int steps = (K16 + 63) / 64, full = K16 / 64;
 
-  // Copy k of this wavefront: block wave + 4 k; its lane's row and chunk.
+  // Copy k of this wavefront: block wave + 4 k (past the last block: that one
+  // again, the same bytes), this lane's row and chunk of it. Chunks past K
+  // (in the last step) are read as the row's first one, and the codes that
+  // came that way are then zeroed in LDS by the lanes that copied them.
   const int row = lane >> 2;
   const int chunk = (lane & 3) ^ (((row >> 1) & 3) ^ ((row >> 3) & 1));
-  const int8_t* const wbase = p.w + n0 * p.ldw;
-  const int8_t* const qbase = p.q + b0 * p.ldq;
   const int rows_n = (int)min((int64_t)(32 * PN), p.N - n0);
   const int rows_b = (int)min((int64_t)(32 * PB), p.B - b0);
+  const int8_t* base[kCopies];
   uint32_t off[kCopies];
+  int to[kCopies];
 #pragma unroll
   for (int k = 0; k < kCopies; ++k) {
-    const int blk = wave + 4 * k;
-    const bool is_w = k < PN / 2;
+    const int blk = min(wave + 4 * k, kBlocks - 1);
+    const bool is_w = blk < 2 * PN;
     const int rr = 16 * (is_w ? blk : blk - 2 * PN) + row;
-    off[k] = is_w ? (uint32_t)min(rr, rows_n - 1) * (uint32_t)p.ldw + 16 * chunk
-                  : (uint32_t)min(rr, rows_b - 1) * (uint32_t)p.ldq + 16 * chunk;
+    base[k] = is_w ? p.w + n0 * p.ldw : p.q + b0 * p.ldq;
+    off[k] = (uint32_t)min(rr, (is_w ? rows_n : rows_b) - 1) * (uint32_t)(is_w ? p.ldw : p.ldq);
+    to[k] = blk * 64;
   }
+  auto lane_at = [&](int s) __attribute__((always_inline)) {
+    const uint32_t at = 64u * (uint32_t)min(s, steps - 1) + 16u * (uint32_t)chunk;
+    return at < (uint32_t)K16 ? at : 0u;
+  };
+  auto copy_one = [&](int k, uint32_t at, uint4* dst) __attribute__((always_inline)) {
+    __builtin_amdgcn_global_load_lds((const void*)(base[k] + (off[k] + at)),
+                                     (__attribute__((address_space(3))) void*)(dst + to[k]), 16, 0, 0);
+  };
   auto copy_step = [&](int s, uint4* dst) __attribute__((always_inline)) {
-    const int at = 64 * min(s, steps - 1);
-    auto copy = [&](const int8_t* from, int k) __attribute__((always_inline)) {
-      __builtin_amdgcn_global_load_lds((const void*)from,
-                                       (__attribute__((address_space(3))) void*)(dst + (wave + 4 * k) * 64),
-                                       16, 0, 0);
-    };
-    if (at + 64 <= K16) {
+    const uint32_t at = lane_at(s);
 #pragma unroll
-      for (int k = 0; k < kCopies; ++k) {
-        const int8_t* src = (k < PN / 2 ? wbase : qbase) + at;
-        copy(src + off[k], k);
-      }
-    } else {
-      // chunks past K: zero codes, against any weights that are there
-      const bool past = at + 16 * chunk >= K16;
+    for (int k = 0; k < kCopies; ++k) copy_one(k, at, dst);
+  };
+  // The step that ends inside its 64 bytes, if one does.
+  const int part = full < steps ? full : -1;
+  auto zero_past = [&](uint4* st) __attribute__((always_inline)) {
 #pragma unroll
-      for (int k = 0; k < kCopies; ++k) {
-        const bool is_w = k < PN / 2;
-        const int8_t* from = (is_w ? wbase : qbase) + off[k] + (past ? -16 * chunk : at);
-        if (!is_w && past) from = reinterpret_cast<const int8_t*>(&kZeroChunk);
-        copy(from, k);
-      }
-    }
+    for (int k = 0; k < kCopies; ++k)
+      if (to[k] >= 2 * PN * 64 && 64 * full + 16 * chunk >= K16) st[to[k] + lane] = make_uint4(0, 0, 0, 0);
   };
   const int rd = 4 * r + (g ^ (((r >> 1) & 3) ^ ((r >> 3) & 1)));   // in 16-byte units
-  auto read_step = [&](const uint4* st, i32x4 (&a)[PN], i32x4 (&c)[PB]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < PN; ++i) a[i] = *reinterpret_cast<const i32x4*>(st + (wn * PN + i) * 64 + rd);
-#pragma unroll
-    for (int j = 0; j < PB; ++j)
-      c[j] = *reinterpret_cast<const i32x4*>(st + (2 * PN + wb * PB + j) * 64 + rd);
-  };
+  const int rd_a = wn * PN * 64 + rd, rd_c = (2 * PN + wb * PB) * 64 + rd;
   auto stage_c = [&](auto ic) __attribute__((always_inline)) -> uint4* {
     constexpr int i = decltype(ic)::value & 3;
     if constexpr (i == 0) return stage0;
@@ -117,53 +120,80 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(Int8Gemm p, int tiles
     else if constexpr (i == 2) return stage2;
     else return stage3;
   };
-  constexpr int kVm = (kStages - 2) * kCopies;        // copies that may be in flight at the barrier
-  constexpr int kWaitVm = (kVm & 15) | ((kVm >> 4) << 14) | (7 << 4) | (15 << 8);
+  constexpr int kWaitVm = (kCopies & 15) | ((kCopies >> 4) << 14) | (7 << 4) | (15 << 8);
   constexpr int kWaitLds0 = (3 << 14) | (7 << 4) | 15;
 
   i32x4 acc[PN][PB];
 #pragma unroll
   for (int i = 0; i < PN; ++i)
 #pragma unroll
-    for (int j = 0; j < PB; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
+    for (int j = 0; j < PB; ++j) mfma_zero(acc[i][j]);
 
   copy_step(0, stage0);
   copy_step(1, stage1);
   copy_step(2, stage2);
   i32x4 a0[PN], c0[PB], a1[PN], c1[PB];
-  __builtin_amdgcn_s_waitcnt(kWaitVm);
+  __builtin_amdgcn_s_waitcnt((2 * kCopies & 15) | ((2 * kCopies >> 4) << 14) | (7 << 4) | (15 << 8));
+  if (part == 0) zero_past(stage0);
+  __builtin_amdgcn_s_waitcnt(kWaitLds0);
   __builtin_amdgcn_s_barrier();
-  read_step(stage0, a0, c0);
+#pragma unroll
+  for (int i = 0; i < PN; ++i) a0[i] = *reinterpret_cast<const i32x4*>(stage0 + rd_a + 64 * i);
+#pragma unroll
+  for (int j = 0; j < PB; ++j) c0[j] = *reinterpret_cast<const i32x4*>(stage0 + rd_c + 64 * j);
 
+  // One step: PN groups of PB products. Each group also issues its share of
+  // the copies of step s + 3 (into the stage of step s - 1, which every
+  // wavefront has read by the barrier) and of the reads of step s + 1's
+  // operands, which are done by the last groups. Spread like this, the
+  // copies never queue up before the products.
   auto do_step = [&](auto sc, int s, i32x4 (&a)[PN], i32x4 (&c)[PB], i32x4 (&an)[PN],
                      i32x4 (&cn)[PB]) __attribute__((always_inline)) {
     constexpr int su = decltype(sc)::value;
-    // The next step's stage (copied two steps ago or earlier), and this
-    // wavefront's reads of this step's.
-    copy_step(s + 3, stage_c(std::integral_constant<int, su + 3>{}));
+    uint4* const fill = stage_c(std::integral_constant<int, su + 3>{});
+    const uint4* const next = stage_c(std::integral_constant<int, su + 1>{});
+    constexpr int kReads = (PN + PB + PN - 3) / (PN - 2);       // per group, done two groups early
+    constexpr int kPer = (kCopies + PN - 1) / PN;
+    const uint32_t at = lane_at(s + 3);
     __builtin_amdgcn_s_waitcnt(kWaitVm);
+    if (s + 1 == part) zero_past(stage_c(std::integral_constant<int, su + 1>{}));
     __builtin_amdgcn_s_waitcnt(kWaitLds0);
     __builtin_amdgcn_s_barrier();
-    read_step(stage_c(std::integral_constant<int, su + 1>{}), an, cn);
 #pragma unroll
-    for (int i = 0; i < PN; ++i)
+    for (int i = 0; i < PN; ++i) {
+#pragma unroll
+      for (int x = i * kReads; x < (i + 1) * kReads; ++x) {
+        if (x < PB) cn[x] = *reinterpret_cast<const i32x4*>(next + rd_c + 64 * x);
+        else if (x < PB + PN) an[x - PB] = *reinterpret_cast<const i32x4*>(next + rd_a + 64 * (x - PB));
+      }
+#pragma unroll
+      for (int k = i * kPer; k < (i + 1) * kPer; ++k)
+        if (k < kCopies) copy_one(k, at, fill);
 #pragma unroll
       for (int j = 0; j < PB; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], c[j], acc[i][j], 0, 0, 0);
+        mfma_acc(acc[i][j], a[i], c[j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
-  int s = 0;
-  for (; s + 4 <= steps; s += 4) {
+  for (int s = 0;;) {
     do_step(std::integral_constant<int, 0>{}, s, a0, c0, a1, c1);
-    do_step(std::integral_constant<int, 1>{}, s + 1, a1, c1, a0, c0);
-    do_step(std::integral_constant<int, 2>{}, s + 2, a0, c0, a1, c1);
-    do_step(std::integral_constant<int, 3>{}, s + 3, a1, c1, a0, c0);
+    if (++s == steps) break;
+    do_step(std::integral_constant<int, 1>{}, s, a1, c1, a0, c0);
+    if (++s == steps) break;
+    do_step(std::integral_constant<int, 2>{}, s, a0, c0, a1, c1);
+    if (++s == steps) break;
+    do_step(std::integral_constant<int, 3>{}, s, a1, c1, a0, c0);
+    if (++s == steps) break;
   }
-  if (s < steps) do_step(std::integral_constant<int, 0>{}, s, a0, c0, a1, c1);
-  if (s + 1 < steps) do_step(std::integral_constant<int, 1>{}, s + 1, a1, c1, a0, c0);
-  if (s + 2 < steps) do_step(std::integral_constant<int, 2>{}, s + 2, a0, c0, a1, c1);
 
   // No copy may still be writing LDS when the workgroup ends.
   __builtin_amdgcn_s_waitcnt(0);
+  acc_ready();
+#pragma unroll
+  for (int i = 0; i < PN; ++i)
+#pragma unroll
+    for (int j = 0; j < PB; ++j) asm volatile("" : "+a"(acc[i][j]));
+  __builtin_amdgcn_sched_barrier(0);
   // Lane (g, r) of tile (i, j) holds weight rows 4 g .. 4 g + 3 of panel i
   // for token r of panel j.
 #pragma unroll
