@@ -86,7 +86,9 @@ __global__ __launch_bounds__(512) void int8_stream_kernel(Int8Gemm p, int tiles_
     i32x4 v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = sum[((t >> 6) * 4 + e) * 64 + (t & 63)];
-    store_int8_sums(p, b, n, p.scale[b], v);
+    float rs[4], bias[4];
+    load_int8_rows(p, n, rs, bias);
+    store_int8_sums(p, b, n, p.scale[b], rs, bias, v);
   }
 }
 

@@ -195,17 +195,55 @@ __global__ __launch_bounds__(256, 1) void int8_tile_kernel(Int8Gemm p, int tiles
     for (int j = 0; j < PB; ++j) asm volatile("" : "+a"(acc[i][j]));
   __builtin_amdgcn_sched_barrier(0);
   // Lane (g, r) of tile (i, j) holds weight rows 4 g .. 4 g + 3 of panel i
-  // for token r of panel j.
+  // for token r of panel j. All scales are loaded before any output is
+  // stored. For bf16 two panels of rows are exchanged between lanes of the
+  // same token (the upper half of one with the lower half of the other, then
+  // odd rows of 16 lanes with even ones) so that lane g holds 8 consecutive
+  // outputs of the 32: a token's four lanes store 64 consecutive bytes.
+  const int64_t nw = n0 + 16 * wn * PN, bw = b0 + 16 * wb * PB + r;
+  float rs[PN][4], bias[PN][4], sb[PB];
+#pragma unroll
+  for (int j = 0; j < PB; ++j) sb[j] = p.scale[min(bw + 16 * j, p.B - 1)];
+#pragma unroll
+  for (int i = 0; i < PN; ++i) load_int8_rows(p, min(nw + 16 * i + 4 * g, p.N - 1), rs[i], bias[i]);
+  if (p.y_bf16 && nw + 16 * PN <= p.N) {
+#pragma unroll
+    for (int j = 0; j < PB; ++j) {
+      const int64_t b = bw + 16 * j;
+      uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + b * p.ldy + nw;
+      uint32_t w[PN][2];
+#pragma unroll
+      for (int i = 0; i < PN; ++i) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fmaf((float)acc[i][j][e], sb[j] * rs[i][e], bias[i][e]);
+        w[i][0] = f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16);
+        w[i][1] = f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16);
+      }
+#pragma unroll
+      for (int i = 0; i + 1 < PN; i += 2) {
+        uint32_t o[4];
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const auto x = __builtin_amdgcn_permlane32_swap(w[i][d], w[i + 1][d], false, false);
+          const auto z = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+          o[d] = z[0];
+          o[2 + d] = z[1];
+        }
+        if (b < p.B) __builtin_memcpy(y + 16 * i + 8 * g, o, 16);
+      }
+      if (PN % 2 != 0 && b < p.B) __builtin_memcpy(y + 16 * (PN - 1) + 4 * g, w[PN - 1], 8);
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < PB; ++j) {
-    const int64_t b = b0 + 16 * (wb * PB + j) + r;
+    const int64_t b = bw + 16 * j;
     if (b >= p.B) continue;
-    const float sb = p.scale[b];
 #pragma unroll
     for (int i = 0; i < PN; ++i) {
-      const int64_t n = n0 + 16 * (wn * PN + i) + 4 * g;
-      if (n >= p.N) continue;
-      store_int8_sums(p, b, n, sb, acc[i][j]);
+      const int64_t n = nw + 16 * i + 4 * g;
+      if (n < p.N) store_int8_sums(p, b, n, sb[j], rs[i], bias[i], acc[i][j]);
     }
   }
 }
