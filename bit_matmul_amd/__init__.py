@@ -19,9 +19,9 @@ from ._lib import (LQ_MULTI_MAX, LQ_ENCODE_MAX_D, LQ_ENCODE_MAX_SMALL_D, LQ_ENCO
                    LQ_ALGO_MFMA_SMALL,
                    LQ_ALGO_VALU, LQ_BF16, LQ_F32, LQ_MAX_D, LQ_MAX_HB, LQ_WS_CONTROL_BYTES,
                    LQ_WS_ERROR_WORD, LQ_NOALLOC_SCRATCH_BYTES, LQ_ERR_DEVICE, LQ_MAX_L, LQError,
-                   LQLayer, LQPlanInfo, LQInt8Layer, LQNormBlockArgs, LQ_ACT_NONE, LQ_ACT_SILU,
+                   LQLayer, LQPlanInfo, LQInt8Layer, LQInt8PlanInfo, LQNormBlockArgs, LQ_ACT_NONE, LQ_ACT_SILU,
                    LQ_ACT_GELU, LQ_ACT_SIGMOID, LQ_ACT_TANH, LQ_NORM_POST, LQ_NORM_PRE,
-                   LQ_NORM_GATE_FIRST, LQ_NORM_ONE_PLUS, LQ_ROW_MAX_K, LQ_INT8_MAX_K)
+                   LQ_NORM_GATE_FIRST, LQ_NORM_ONE_PLUS, LQ_ROW_MAX_K, LQ_INT8_MAX_K, LQ_INT8_MAX_LD)
 
 __all__ = [
     "lq_version", "lq_packed_size", "lq_pack_signs", "lq_unpack_signs", "lq_hadamard_scale",
@@ -38,10 +38,11 @@ __all__ = [
     "lq_linear_plan", "lq_sign_gemm_plan", "lq_workspace_status", "lq_debug_fused_timeout",
     "LQ_ERR_DEVICE", "LQ_MAX_L", "LQPlanInfo",
     "lq_quant_rows", "int8_layer_struct", "lq_int8_gemm_workspace_size", "lq_int8_gemm",
-    "lq_int8_linear_workspace_size", "lq_int8_linear", "lq_norm_block", "LQInt8Layer",
+    "lq_int8_linear_workspace_size", "lq_int8_linear", "lq_int8_gemm_plan", "lq_norm_block",
+    "LQInt8Layer", "LQInt8PlanInfo",
     "LQNormBlockArgs", "LQ_ACT_NONE", "LQ_ACT_SILU", "LQ_ACT_GELU", "LQ_ACT_SIGMOID",
     "LQ_ACT_TANH", "LQ_NORM_POST", "LQ_NORM_PRE", "LQ_NORM_GATE_FIRST", "LQ_NORM_ONE_PLUS",
-    "LQ_ROW_MAX_K", "LQ_INT8_MAX_K",
+    "LQ_ROW_MAX_K", "LQ_INT8_MAX_K", "LQ_INT8_MAX_LD",
 ]
 
 _DTYPES = {torch.float32: LQ_F32, torch.bfloat16: LQ_BF16}
@@ -400,6 +401,13 @@ def lq_int8_gemm(layer: LQInt8Layer, q, scale, B, y, ws=None, stream=None) -> No
     _check(_lib.LIB.lq_int8_gemm(ctypes.byref(layer), qp, ldq, _vec(scale, "scale", B), B, yp,
                                  _dtype(y, "y"), ldy, _opt(ws, "ws"), ws_bytes, _stream(stream)),
            "lq_int8_gemm")
+
+
+def lq_int8_gemm_plan(layer: LQInt8Layer, B) -> dict:
+    """Tile and split of the reduction that lq_int8_gemm would use."""
+    info = LQInt8PlanInfo()
+    _check(_lib.LIB.lq_int8_gemm_plan(ctypes.byref(layer), B, ctypes.byref(info)), "lq_int8_gemm_plan")
+    return {f: getattr(info, f) for f, _ in LQInt8PlanInfo._fields_}
 
 
 def lq_int8_linear_workspace_size(layer: LQInt8Layer, B, xtype) -> int:

@@ -25,6 +25,7 @@ LQ_ACT_NONE, LQ_ACT_SILU, LQ_ACT_GELU, LQ_ACT_SIGMOID, LQ_ACT_TANH = range(5)
 LQ_NORM_POST, LQ_NORM_PRE, LQ_NORM_GATE_FIRST, LQ_NORM_ONE_PLUS = 1, 2, 4, 8
 LQ_ROW_MAX_K = 65536
 LQ_INT8_MAX_K = 131071
+LQ_INT8_MAX_LD = 1 << 23
 LQ_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 # Every symbol include/lq.h declares.
@@ -39,6 +40,7 @@ EXPORTS = [
     "lq_workspace_status", "lq_debug_fused_timeout", "lq_encode_pinv_workspace_size",
     "lq_encode_pinv", "lq_quant_rows", "lq_int8_gemm_workspace_size", "lq_int8_gemm",
     "lq_int8_linear_workspace_size", "lq_int8_linear", "lq_norm_block",
+    "lq_int8_gemm_plan",
 ]
 
 
@@ -65,6 +67,11 @@ class LQInt8Layer(ctypes.Structure):
         ("N", c_int64), ("K", c_int64), ("ldw", c_int64), ("hb", c_int32), ("reserved", c_int32),
         ("w", c_void_p), ("c", c_void_p), ("row_scale", c_void_p), ("bias", c_void_p),
     ]
+
+
+class LQInt8PlanInfo(ctypes.Structure):
+    """Mirror of ``struct lq_int8_plan_info``."""
+    _fields_ = [("rows", c_int32), ("tokens", c_int32), ("ksplit", c_int32), ("workgroups", c_int32)]
 
 
 class LQNormBlockArgs(ctypes.Structure):
@@ -138,6 +145,7 @@ def _load():
         "lq_int8_linear_workspace_size": (c_int, [POINTER(LQInt8Layer), i64, c_int, POINTER(sz)]),
         "lq_int8_linear": (c_int, [POINTER(LQInt8Layer), vp, c_int, i64, i64, vp, c_int, i64, vp,
                                    sz, vp]),
+        "lq_int8_gemm_plan": (c_int, [POINTER(LQInt8Layer), i64, POINTER(LQInt8PlanInfo)]),
         "lq_norm_block": (c_int, [POINTER(LQNormBlockArgs), vp]),
     }
     for name, (res, args) in protos.items():

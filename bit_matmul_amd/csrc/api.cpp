@@ -973,6 +973,9 @@ lq_status lq_profile_events(void* const* starts, void* const* stops, int32_t cou
 
 namespace {
 
+constexpr int64_t kMaxInt8N = int64_t(1) << 28;      // outputs of an 8-bit layer
+constexpr int64_t kMaxInt8Out = int64_t(1) << 36;    // B * N
+
 bool valid_act(int32_t act) { return act >= LQ_ACT_NONE && act <= LQ_ACT_TANH; }
 bool aligned_to(const void* p, lq_dtype t) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (t == LQ_F32 ? 3u : 1u)) == 0;
@@ -991,6 +994,7 @@ lq_status check_ld(int64_t ld, int64_t width) {
 }
 lq_status check_q(const int8_t* q, int64_t ldq, int64_t K) {
   if (!aligned16(q) || ldq % 16 != 0) return LQ_ERR_INVALID_ARG;
+  if (ldq > LQ_INT8_MAX_LD) return LQ_ERR_UNSUPPORTED;
   return check_ld(ldq, round16(K));
 }
 lq_status check_hb(int64_t K, int32_t hb) {
@@ -1001,27 +1005,40 @@ lq_status check_hb(int64_t K, int32_t hb) {
 
 lq_status check_int8_layer(const lq_int8_layer* l, int64_t B, int64_t max_k) {
   if (l == nullptr || l->reserved != 0 || l->N < 0) return LQ_ERR_INVALID_ARG;
-  if (l->N > kMaxDim) return LQ_ERR_UNSUPPORTED;
+  if (l->N > kMaxInt8N) return LQ_ERR_UNSUPPORTED;
   lq_status s = check_rows(B, l->K, max_k);
   if (s == LQ_OK) s = check_hb(l->K, l->hb);
   if (s == LQ_OK && l->ldw % 16 != 0) s = LQ_ERR_INVALID_ARG;
   if (s == LQ_OK) s = check_ld(l->ldw, round16(l->K));
-  if (s == LQ_OK && !mul_ok(B, l->N, kMaxElems)) s = LQ_ERR_UNSUPPORTED;
+  if (s == LQ_OK && (l->ldw > LQ_INT8_MAX_LD || !mul_ok(B, l->N, kMaxInt8Out))) s = LQ_ERR_UNSUPPORTED;
   return s;
+}
+
+lq::Int8Plan int8_plan(const lq_int8_layer* l, int64_t B) {
+  return lq::plan_int8(B, l->N, l->K, device_cus());
+}
+// The product's workspace: the control area (left as it is), the parts' sums.
+size_t int8_gemm_bytes(const lq::Int8Plan& plan) {
+  return plan.ksplit > 1 ? align_up(lq::kControlBytes) + align_up(plan.partial_bytes) : 0;
+}
+int* int8_partial(const lq::Int8Plan& plan, void* ws, size_t off) {
+  return plan.ksplit > 1 ? reinterpret_cast<int*>(static_cast<char*>(ws) + off) : nullptr;
 }
 
 // The pieces of lq_int8_linear's workspace, behind the control area.
 struct Int8Ws {
-  size_t off_q, off_scale, off_gemm, total;
+  lq::Int8Plan plan;
+  size_t off_q, off_scale, off_partial, total;
   int64_t ldq;
 };
 Int8Ws int8_ws(const lq_int8_layer* l, int64_t B) {
   Int8Ws w;
+  w.plan = int8_plan(l, B);
   w.ldq = round16(l->K);
   w.off_q = align_up(lq::kControlBytes);
   w.off_scale = w.off_q + align_up((size_t)B * w.ldq);
-  w.off_gemm = w.off_scale + align_up((size_t)B * sizeof(float));
-  w.total = w.off_gemm;
+  w.off_partial = w.off_scale + align_up((size_t)B * sizeof(float));
+  w.total = w.off_partial + align_up(w.plan.partial_bytes);
   return w;
 }
 
@@ -1072,23 +1089,34 @@ lq_status lq_int8_gemm_workspace_size(const lq_int8_layer* layer, int64_t B, siz
   if (bytes == nullptr) return LQ_ERR_INVALID_ARG;
   lq_status s = check_int8_layer(layer, B, LQ_INT8_MAX_K);
   if (s != LQ_OK) return s;
-  *bytes = 0;
+  *bytes = B == 0 || layer->N == 0 ? 0 : int8_gemm_bytes(int8_plan(layer, B));
+  return LQ_OK;
+}
+
+lq_status lq_int8_gemm_plan(const lq_int8_layer* layer, int64_t B, lq_int8_plan_info* info) {
+  if (info == nullptr) return LQ_ERR_INVALID_ARG;
+  lq_status s = check_int8_layer(layer, B, LQ_INT8_MAX_K);
+  if (s != LQ_OK) return s;
+  if (B < 1 || layer->N < 1) return LQ_ERR_INVALID_ARG;
+  const lq::Int8Plan p = int8_plan(layer, B);
+  *info = {32 * p.pn, 32 * p.pb, p.ksplit, p.tiles * p.ksplit};
   return LQ_OK;
 }
 
 lq_status lq_int8_gemm(const lq_int8_layer* layer, const int8_t* q, int64_t ldq,
                        const float* scale, int64_t B, void* y, lq_dtype ytype, int64_t ldy,
                        void* ws, size_t ws_bytes, void* stream) {
-  size_t need = 0;
-  lq_status s = lq_int8_gemm_workspace_size(layer, B, &need);
+  lq_status s = check_int8_layer(layer, B, LQ_INT8_MAX_K);
   if (s != LQ_OK) return s;
   if (B == 0 || layer->N == 0) return LQ_OK;
+  const lq::Int8Plan plan = int8_plan(layer, B);
   s = check_gemm_ptrs(layer, y, ytype, ldy);
   if (s == LQ_OK && !aligned_to(scale, LQ_F32)) s = LQ_ERR_INVALID_ARG;
   if (s == LQ_OK) s = check_q(q, ldq, layer->K);
-  if (s == LQ_OK) s = check_ws(ws, ws_bytes, need);
+  if (s == LQ_OK) s = check_ws(ws, ws_bytes, int8_gemm_bytes(plan));
   if (s != LQ_OK) return s;
-  return hip_status(lq::launch_int8_gemm(gemm_args(layer, q, ldq, scale, B, y, ytype, ldy),
+  return hip_status(lq::launch_int8_gemm(gemm_args(layer, q, ldq, scale, B, y, ytype, ldy), plan,
+                                         int8_partial(plan, ws, align_up(lq::kControlBytes)),
                                          (hipStream_t)stream));
 }
 
@@ -1104,17 +1132,17 @@ lq_status lq_int8_linear_workspace_size(const lq_int8_layer* layer, int64_t B, l
 lq_status lq_int8_linear(const lq_int8_layer* layer, const void* x, lq_dtype xtype, int64_t ldx,
                          int64_t B, void* y, lq_dtype ytype, int64_t ldy, void* ws,
                          size_t ws_bytes, void* stream) {
-  size_t need = 0;
-  lq_status s = lq_int8_linear_workspace_size(layer, B, xtype, &need);
+  if (!valid_dtype(xtype)) return LQ_ERR_INVALID_ARG;
+  lq_status s = check_int8_layer(layer, B, LQ_ROW_MAX_K);
   if (s != LQ_OK) return s;
   if (B == 0 || layer->N == 0) return LQ_OK;
+  const Int8Ws w = int8_ws(layer, B);
   s = check_ld(ldx, layer->K);
   if (s == LQ_OK && !aligned_to(x, xtype)) s = LQ_ERR_INVALID_ARG;
   if (s == LQ_OK && layer->c != nullptr && !aligned_to(layer->c, LQ_F32)) s = LQ_ERR_INVALID_ARG;
   if (s == LQ_OK) s = check_gemm_ptrs(layer, y, ytype, ldy);
-  if (s == LQ_OK) s = check_ws(ws, ws_bytes, need);
+  if (s == LQ_OK) s = check_ws(ws, ws_bytes, w.total);
   if (s != LQ_OK) return s;
-  const Int8Ws w = int8_ws(layer, B);
   char* base = static_cast<char*>(ws);
   int8_t* q = reinterpret_cast<int8_t*>(base + w.off_q);
   float* scale = reinterpret_cast<float*>(base + w.off_scale);
@@ -1123,7 +1151,8 @@ lq_status lq_int8_linear(const lq_int8_layer* layer, const void* x, lq_dtype xty
   fill_hb(&p, layer->hb);
   s = hip_status(lq::launch_quant_rows(p, (hipStream_t)stream));
   if (s != LQ_OK) return s;
-  return hip_status(lq::launch_int8_gemm(gemm_args(layer, q, w.ldq, scale, B, y, ytype, ldy),
+  return hip_status(lq::launch_int8_gemm(gemm_args(layer, q, w.ldq, scale, B, y, ytype, ldy), w.plan,
+                                         int8_partial(w.plan, ws, w.off_partial),
                                          (hipStream_t)stream));
 }
 

@@ -1,4 +1,4 @@
-// Device helpers of the 8-bit products (int8_stream.hip, int8_tile.hip).
+// Device helpers of the 8-bit product (int8_gemm.hip).
 #pragma once
 
 #include "lq_internal.h"

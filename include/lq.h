@@ -404,11 +404,12 @@ typedef enum lq_act {
 
 #define LQ_ROW_MAX_K 65536    /* longest row of lq_quant_rows and lq_norm_block */
 #define LQ_INT8_MAX_K 131071  /* longest sum of products of bytes that 32 bits hold */
+#define LQ_INT8_MAX_LD (1 << 23) /* most bytes from one 8-bit row to the next */
 
 /* One 8-bit linear layer (all pointers device, caller-owned). Layers that
  * read the same input are one layer of more rows. */
 typedef struct lq_int8_layer {
-  int64_t N;                 /* output features */
+  int64_t N;                 /* output features, at most 2^28, and B * N at most 2^36 */
   int64_t K;                 /* input features */
   int64_t ldw;               /* bytes from one row of w to the next, a multiple of 16 */
   int32_t hb;                /* Hadamard block of T, as in lq_layer; 1: none */
@@ -427,7 +428,7 @@ typedef struct lq_int8_layer {
  * that of the exact quotient. Errors: INVALID_ARG for a NULL or misaligned pointer, a
  * negative size, K < 1, ld below K, ldq not a multiple of 16, an unknown act
  * or dtype, hb not a power of two or not a divisor of K; UNSUPPORTED for
- * K > LQ_ROW_MAX_K or hb > LQ_MAX_HB.
+ * K > LQ_ROW_MAX_K, hb > LQ_MAX_HB or ldq > LQ_INT8_MAX_LD.
  */
 lq_status lq_quant_rows(const void* x, lq_dtype xtype, int64_t ldx, const void* gate, int64_t ldg,
                         lq_act act, int64_t B, int64_t K, int32_t hb, const float* c, int8_t* q,
@@ -438,14 +439,30 @@ lq_status lq_quant_rows(const void* x, lq_dtype xtype, int64_t ldx, const void* 
  * layer's weights: y, B rows of N in ytype, ldy elements apart. The layer's
  * hb and c are not used. y = (float)sum * (scale * row_scale) + bias in fp32,
  * rounded once to ytype. ws: device workspace of at least
- * lq_int8_gemm_workspace_size bytes (may be NULL when that size is 0).
- * Errors: INVALID_ARG as above; UNSUPPORTED for K > LQ_INT8_MAX_K;
+ * lq_int8_gemm_workspace_size bytes (may be NULL when that size is 0), whose
+ * control area is left as it is and whose rest needs no preparation.
+ * Errors: INVALID_ARG as above; UNSUPPORTED for K > LQ_INT8_MAX_K, ldw or
+ * ldq > LQ_INT8_MAX_LD, or more outputs than said above;
  * WORKSPACE for a missing or short workspace.
  */
 lq_status lq_int8_gemm_workspace_size(const lq_int8_layer* layer, int64_t B, size_t* bytes);
 lq_status lq_int8_gemm(const lq_int8_layer* layer, const int8_t* q, int64_t ldq,
                        const float* scale, int64_t B, void* y, lq_dtype ytype, int64_t ldy,
                        void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * How lq_int8_gemm would run, without running it (host only). Errors: as
+ * lq_int8_gemm_workspace_size, INVALID_ARG for a NULL info or nothing to do.
+ */
+typedef struct lq_int8_plan_info {
+  int32_t rows;              /* weight rows of a workgroup's tile */
+  int32_t tokens;            /* tokens of a workgroup's tile */
+  int32_t ksplit;            /* workgroups that share a tile, each with a part
+                                of the reduction (1 = none; else a second
+                                launch adds their sums) */
+  int32_t workgroups;        /* of the product's launch that have work */
+} lq_int8_plan_info;
+lq_status lq_int8_gemm_plan(const lq_int8_layer* layer, int64_t B, lq_int8_plan_info* info);
 
 /*
  * The whole 8-bit layer: lq_quant_rows of x with the layer's T, then

@@ -8,7 +8,7 @@ import pytest
 from bit_matmul_amd._lib import (LIB, LQ_ACT_NONE, LQ_BF16, LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED,
                                  LQ_ERR_WORKSPACE, LQ_F32, LQ_INT8_MAX_K, LQ_NORM_POST,
                                  LQ_NORM_PRE, LQ_OK, LQ_ROW_MAX_K, LQ_WS_CONTROL_BYTES,
-                                 LQInt8Layer, LQNormBlockArgs)
+                                 LQInt8Layer, LQInt8PlanInfo, LQNormBlockArgs)
 
 P = 0x100000            # fake, 16-byte aligned device address
 INV, UNS = LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED
@@ -29,7 +29,7 @@ def quant(**kw):
     (dict(K=0), INV), (dict(hb=0), INV), (dict(hb=3), INV), (dict(hb=128), INV),
     (dict(K=4096, ldx=4096, ldq=4096, hb=2048), UNS), (dict(c=P + 2), INV), (dict(q=None), INV),
     (dict(q=P + 8), INV), (dict(ldq=72), INV), (dict(K=65, ldx=65), INV), (dict(scale=None), INV),
-    (dict(scale=P + 2), INV), (dict(B=(1 << 20) + 1), UNS),
+    (dict(scale=P + 2), INV), (dict(B=(1 << 20) + 1), UNS), (dict(ldq=(1 << 23) + 16), UNS),
     (dict(K=LQ_ROW_MAX_K + 1, ldx=LQ_ROW_MAX_K + 1, ldq=LQ_ROW_MAX_K + 16), UNS),
     (dict(B=0), LQ_OK), (dict(B=0, x=None, q=None, scale=None), LQ_OK),
 ])
@@ -45,13 +45,18 @@ def layer(**kw):
 LAYERS = [
     (dict(N=-1), INV), (dict(K=0), INV), (dict(ldw=48), INV), (dict(ldw=72), INV),
     (dict(K=65), INV), (dict(hb=3), INV), (dict(hb=0), INV), (dict(reserved=1), INV),
-    (dict(K=LQ_INT8_MAX_K + 1, ldw=LQ_INT8_MAX_K + 1), UNS), (dict(N=1 << 31), UNS),
+    (dict(K=LQ_INT8_MAX_K + 1, ldw=LQ_INT8_MAX_K + 1), UNS), (dict(N=(1 << 28) + 1), UNS),
+    (dict(ldw=(1 << 23) + 16), UNS), (dict(N=1 << 28, K=16), LQ_OK),
 ]
 
 
 @pytest.mark.parametrize("kw,status", LAYERS)
 def test_int8_layer_validation(kw, status):
     n = ctypes.c_size_t(77)
+    if status == LQ_OK:
+        assert LIB.lq_int8_gemm_workspace_size(layer(**kw), 2, ctypes.byref(n)) == status
+        assert LIB.lq_int8_gemm_workspace_size(layer(**kw), 1 << 10, ctypes.byref(n)) == UNS
+        return
     assert LIB.lq_int8_gemm_workspace_size(layer(**kw), 2, ctypes.byref(n)) == status
     assert LIB.lq_int8_linear_workspace_size(layer(**kw), 2, LQ_F32, ctypes.byref(n)) == status
     assert LIB.lq_int8_gemm(layer(**kw), P, 64, P, 2, P, LQ_F32, 32, None, 0, None) == status
@@ -90,6 +95,38 @@ GEMM = dict(q=P, ldq=64, scale=P, B=2, y=P, ytype=LQ_BF16, ldy=32, ws=None, wsb=
 def test_int8_gemm_validation(kw, lkw, status):
     a = {**GEMM, **kw}
     assert LIB.lq_int8_gemm(layer(**lkw), *(a[k] for k in GEMM), None) == status
+
+
+def test_int8_gemm_plan():
+    info = LQInt8PlanInfo()
+    assert LIB.lq_int8_gemm_plan(layer(), 2, None) == INV
+    assert LIB.lq_int8_gemm_plan(layer(), 0, ctypes.byref(info)) == INV
+    assert LIB.lq_int8_gemm_plan(layer(N=0), 2, ctypes.byref(info)) == INV
+    assert LIB.lq_int8_gemm_plan(layer(reserved=2), 2, ctypes.byref(info)) == INV
+    n = ctypes.c_size_t()
+    for B, N, K in ((1, 32, 64), (16, 8192, 28672), (2048, 8192, 28672), (3, 1 << 28, 16), (1 << 20, 1 << 16, 16)):
+        lay = layer(N=N, K=K, ldw=K)
+        assert LIB.lq_int8_gemm_plan(lay, B, ctypes.byref(info)) == LQ_OK
+        tiles = -(-N // info.rows) * -(-B // info.tokens)
+        assert info.workgroups == tiles * info.ksplit < 1 << 24
+        assert 1 <= info.ksplit <= -(-K // 128)
+        assert LIB.lq_int8_gemm_workspace_size(lay, B, ctypes.byref(n)) == LQ_OK
+        # every part's sums, 4 bytes each, behind the control area
+        assert (n.value == 0) == (info.ksplit == 1)
+        if info.ksplit > 1:
+            assert n.value >= LQ_WS_CONTROL_BYTES + 4 * info.workgroups * info.rows * info.tokens
+
+
+def test_int8_gemm_workspace_is_checked():
+    lay = layer(N=8192, K=28672, ldw=28672)
+    n = ctypes.c_size_t()
+    assert LIB.lq_int8_gemm_workspace_size(lay, 16, ctypes.byref(n)) == LQ_OK and n.value > 0
+
+    def f(ws, size):
+        return LIB.lq_int8_gemm(lay, P, 28672, P, 16, P, LQ_F32, 8192, ws, size, None)
+    assert f(None, 0) == LQ_ERR_WORKSPACE
+    assert f(P, n.value - 1) == LQ_ERR_WORKSPACE
+    assert f(P + 8, n.value) == INV
 
 
 def test_int8_linear_validation():

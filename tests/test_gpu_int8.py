@@ -317,6 +317,47 @@ def test_int8_gemm_largest_sum(lq, B):
     assert torch.all(y > 0)
 
 
+# (B, N, K, rows and tokens of the tile, whether the reduction is split)
+VARIANTS = [
+    (3, 1000, 700, 64, 32, False), (1, 500, 3001, 64, 32, True), (129, 10001, 48, 64, 64, False),
+    (1500, 16, 12001, 64, 64, True), (65, 14000, 48, 64, 128, False), (1100, 100, 12001, 64, 128, True),
+    (129, 14000, 48, 128, 128, False), (65, 6000, 12001, 128, 128, True), (257, 14000, 300, 128, 256, False),
+    (400, 5000, 12001, 128, 256, True), (513, 14000, 700, 192, 256, False), (513, 4000, 12001, 192, 256, True),
+    (257, 14000, 48, 224, 256, False), (257, 14000, 12001, 224, 256, True), (1500, 10001, 48, 256, 256, False),
+    (400, 10001, 12001, 256, 256, True),
+]
+
+
+@pytest.mark.parametrize("B,N,K,rows,tokens,split", VARIANTS)
+def test_int8_gemm_every_tile(lq, B, N, K, rows, tokens, split):
+    """Each tile, with and without a split reduction, on sizes that end inside tiles and steps: some
+    tokens and outputs (the first and last tiles among them) against the oracle, bf16 and fp32."""
+    rng = np.random.default_rng(B + N + K)
+    buf = torch.randint(-128, 128, (N, pad16(K)), dtype=torch.int8, device=DEV,
+                        generator=torch.Generator(DEV).manual_seed(B))
+    w = buf[:, :K]
+    r, bias = randn(rng, N).abs() * 1e-3, randn(rng, N)
+    layer = lq.int8_layer_struct(N, K, w, r, bias=bias)
+    plan = lq.lq_int8_gemm_plan(layer, B)
+    assert (plan["rows"], plan["tokens"], plan["ksplit"] > 1) == (rows, tokens, split), plan
+    q = make_q(rng, B, K)
+    scale = randn(rng, B).abs()
+    bs = np.unique(np.concatenate([np.arange(min(B, 20)), rng.integers(0, B, 30), np.arange(max(0, B - 20), B)]))
+    ns = np.unique(np.concatenate([np.arange(min(N, 70)), rng.integers(0, N, 200), np.arange(max(0, N - 270), N)]))
+    want = ref.product(q.cpu().numpy()[bs], host64(scale)[bs], w[torch.from_numpy(ns).to(DEV)].cpu().numpy(),
+                       host64(r)[ns], host64(bias)[ns])
+    for dtype in (F32, BF):
+        out = torch.full((B + 2, N), 9.0, dtype=dtype, device=DEV)
+        note(f"lq_int8_gemm B={B} N={N} K={K} y={dtype} {plan}")
+        lq.lq_int8_gemm(layer, q, scale, B, out[1:B + 1], garbage(lq.lq_int8_gemm_workspace_size(layer, B)))
+        torch.cuda.synchronize()
+        assert torch.all(out[0] == 9.0) and torch.all(out[B + 1] == 9.0)
+        y = out[1:B + 1]
+        assert torch.isfinite(y).all()
+        check_product(y[torch.from_numpy(bs).to(DEV)][:, torch.from_numpy(ns).to(DEV)], want,
+                      bias[torch.from_numpy(ns).to(DEV)], dtype)
+
+
 def test_int8_gemm_scales_zero_and_nan(lq):
     rng = np.random.default_rng(2)
     for B in (3, 150):
