@@ -73,9 +73,14 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return _DTYPES[t.dtype]
 
 
+# The handle of a device's current stream, without a stream object around it
+# (that object costs 3 us of a call's 10).
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -326,14 +331,16 @@ def _rows(t, name: str, B: int, width: int):
     dense: a slice of a wider tensor is taken as it is."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a GPU tensor of two dimensions")
-    if t.size(0) < B or t.size(1) < width:
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if rows < B or cols < width:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {B} rows of {width} are needed")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    if width > 1 and t.stride(1) != 1:
+    if step != 1 and width > 1:
         raise ValueError(f"{name}'s rows must be dense")
     # (a single row's stride says nothing)
-    return t.data_ptr(), t.stride(0) if t.size(0) > 1 else max(t.stride(0), width)
+    return t.data_ptr(), ld if rows > 1 or ld > width else width
 
 
 def _rows8(t, name: str, B: int, K: int):
@@ -342,11 +349,10 @@ def _rows8(t, name: str, B: int, K: int):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int8:
         raise ValueError(f"{name} must be an int8 tensor")
     ptr, ld = _rows(t, name, B, K)
-    padded = -(-K // 16) * 16
+    padded = (K + 15) & -16
     if t.size(0) == 1:
-        ld = max(padded, -(-ld // 16) * 16)
-    end = t.storage_offset() + (B - 1) * ld + padded
-    if B > 0 and end > t.untyped_storage().nbytes():
+        ld = max(padded, (ld + 15) & -16)
+    if B > 0 and t.storage_offset() + (B - 1) * ld + padded > t.untyped_storage().nbytes():
         raise ValueError(f"{name}'s last row must be padded to a multiple of 16 bytes")
     return ptr, ld
 
@@ -357,9 +363,10 @@ def _vec(t, name: str, n: int):
         return None
     if t.dtype != torch.float32 or t.numel() < n:
         raise ValueError(f"{name} must be {n} float32 values")
-    if t.device.index != torch.cuda.current_device():
+    ptr = _dev(t, name)
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return _dev(t, name)
+    return ptr
 
 
 def lq_quant_rows(x, B, K, q, scale, gate=None, act=LQ_ACT_NONE, hb=1, c=None, stream=None) -> None:
@@ -433,34 +440,37 @@ def lq_norm_block(B, K, y=None, gate=None, act=LQ_ACT_NONE, gate_first=False, po
                   one_plus=False, eps=1e-5, a=None, q=None, scale=None, stream=None) -> None:
     """The norms after and before a block with its gate and scaled residual
     (lq.h gives the formulas). gate: rows as y, or one vector of K for all."""
-    p = LQNormBlockArgs(B=B, K=K, act=act, alpha=alpha, eps=eps)
+    yp = gp = hp = hop = ap = qp = None
+    ldy = ldg = ldh = ldho = lda = ldq = yt = ht = at = 0
     if y is not None:
-        p.ytype = _dtype(y, "y")
-        p.y, p.ldy = _rows(y, "y", B, K)
+        yt = _dtype(y, "y")
+        yp, ldy = _rows(y, "y", B, K)
     if gate is not None:
         if y is None or gate.dtype != y.dtype:
             raise ValueError("gate must have y's dtype")
         if gate.dim() == 1:
-            if gate.numel() < K or gate.device.index != torch.cuda.current_device():
+            if gate.numel() < K or gate.get_device() != torch.cuda.current_device():
                 raise ValueError(f"gate must hold {K} values on the current device")
-            p.gate, p.ldg = _dev(gate, "gate"), 0
+            gp = _dev(gate, "gate")
         else:
-            p.gate, p.ldg = _rows(gate, "gate", B, K)
+            gp, ldg = _rows(gate, "gate", B, K)
     if h is not None:
-        p.htype = _dtype(h, "h")
-        p.h, p.ldh = _rows(h, "h", B, K)
+        ht = _dtype(h, "h")
+        hp, ldh = _rows(h, "h", B, K)
     if h_out is not None:
         if h is not None and h_out.dtype != h.dtype:
             raise ValueError("h_out must have h's dtype")
-        p.htype = _dtype(h_out, "h_out")
-        p.h_out, p.ldh_out = _rows(h_out, "h_out", B, K)
+        ht = _dtype(h_out, "h_out")
+        hop, ldho = _rows(h_out, "h_out", B, K)
     if a is not None:
-        p.atype = _dtype(a, "a")
-        p.a, p.lda = _rows(a, "a", B, K)
+        at = _dtype(a, "a")
+        ap, lda = _rows(a, "a", B, K)
     if q is not None:
-        p.q, p.ldq = _rows8(q, "q", B, K)
-    p.scale = _vec(scale, "scale", B)
-    p.w_post, p.w_pre = _vec(w_post, "w_post", K), _vec(w_pre, "w_pre", K)
-    p.flags = ((LQ_NORM_POST if post else 0) | (LQ_NORM_PRE if pre else 0) |
-               (LQ_NORM_GATE_FIRST if gate_first else 0) | (LQ_NORM_ONE_PLUS if one_plus else 0))
+        qp, ldq = _rows8(q, "q", B, K)
+    flags = ((LQ_NORM_POST if post else 0) | (LQ_NORM_PRE if pre else 0) |
+             (LQ_NORM_GATE_FIRST if gate_first else 0) | (LQ_NORM_ONE_PLUS if one_plus else 0))
+    # (in the order of the struct's fields)
+    p = LQNormBlockArgs(B, K, yp, gp, _vec(w_post, "w_post", K), hp, hop, _vec(w_pre, "w_pre", K), ap, qp,
+                        _vec(scale, "scale", B), ldy, ldg, ldh, ldho, lda, ldq, yt, ht, at, act, alpha, eps,
+                        flags, 0)
     _check(_lib.LIB.lq_norm_block(ctypes.byref(p), _stream(stream)), "lq_norm_block")
