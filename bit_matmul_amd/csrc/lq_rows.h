@@ -4,9 +4,10 @@
 // Layout: the row is cut into blocks of 1024 values; wavefront w of W takes
 // blocks w, w + W, ... (C of them). Of a block, lane l holds the values
 // 8 l .. 8 l + 7 and 512 + 8 l .. 512 + 8 l + 7: a wavefront's loads are
-// consecutive 16-byte pieces, its 8-bit stores consecutive 8-byte ones, and
-// the index bits of a block are three register bits, six lane bits and one
-// register bit, so a Hadamard block of up to 1024 needs no LDS.
+// consecutive 16-byte pieces in the order of its lanes (pieces exchanged
+// within 64 bytes loaded a third slower), its 8-bit stores consecutive 8-byte
+// ones, and the index bits of a block are three register bits, six lane bits
+// and one register bit, so a Hadamard block of up to 1024 needs no LDS.
 #pragma once
 
 #include "lq_internal.h"
@@ -19,59 +20,85 @@ constexpr int kRowMaxWaves = 16;
 constexpr int kRowMaxC = 4;
 constexpr int64_t kRowMaxK = (int64_t)kRowBlock * kRowMaxWaves * kRowMaxC;
 
-// Values p[0..7] as floats, those past n (n may be <= 0) as zero. p needs
-// only its element's alignment: gfx950's global loads take any byte address,
-// and one 16-byte load is one instruction for an odd row stride too.
+// Piece j (0, 1) of a thread's block i begins at column row_col(i, j), the
+// same for the wavefront, plus row_lane8(); row_whole: a wavefront's C blocks
+// lie inside the row, so that none of its pieces is cut.
+__device__ __forceinline__ int row_col(int i, int j) {
+  return (wave_id() + i * ((int)blockDim.x >> 6)) * kRowBlock + 512 * j;
+}
+__device__ __forceinline__ uint32_t row_lane8() { return 8u * (threadIdx.x & 63u); }
+template <int C>
+__device__ __forceinline__ bool row_whole(int K) {
+  return (wave_id() + (C - 1) * ((int)blockDim.x >> 6) + 1) * kRowBlock <= K;
+}
+
+// A piece of 8 values as it lies in memory. Loads fill these and nothing
+// more, so that a wavefront has all of its loads in flight: converted where
+// they are loaded (behind a test for the row's end or for a tensor that may
+// be missing), each would wait for its own.
 template <bool kBF16>
-__device__ __forceinline__ void load_row8(const void* base, int64_t at, int n, float (&v)[8]) {
-  if constexpr (kBF16) {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at;
-    if (n >= 8) {
-      uint32_t w[4];
-      __builtin_memcpy(w, p, 16);
+struct RowPiece {
+  uint32_t w[kBF16 ? 4 : 8];
+  __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
+    for (int i = 0; i < 8; ++i)
+      v[i] = __uint_as_float(!kBF16 ? w[i] : i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+};
+// The piece at column col (of the wavefront) of a row of K values, those past
+// K as zero. The row needs only its element's alignment: gfx950's global
+// loads take any byte address, and 16 bytes are one load for an odd row
+// stride too. (A scalar address plus a lane's offset: vector addresses of
+// every piece of every tensor would take most of a long row's registers.)
+template <bool kBF16>
+__device__ __forceinline__ void load_piece(RowPiece<kBF16>& p, const void* row, int col, int K, bool whole) {
+  constexpr uint32_t kSize = kBF16 ? 2 : 4;
+  const char* from = reinterpret_cast<const char*>(row) + (int64_t)col * kSize;
+  const uint32_t lane = row_lane8() * kSize;
+  if (whole) {
+    __builtin_memcpy(p.w, from + lane, sizeof(p.w));
+    return;
+  }
+  const int n = K - col - (int)row_lane8();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? bf16_bits_to_f32(p[i]) : 0.0f;
-    }
+  for (int i = 0; i < (kBF16 ? 4 : 8); ++i) p.w[i] = 0;
+  if (n >= 8) {
+    __builtin_memcpy(p.w, from + lane, sizeof(p.w));
   } else {
-    const float* p = reinterpret_cast<const float*>(base) + at;
-    if (n >= 8) {
-      __builtin_memcpy(v, p, 32);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
-    }
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (kBF16) p.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(from + lane)[i] << (16 * (i & 1));
+        else p.w[i] = reinterpret_cast<const uint32_t*>(from + lane)[i];
+      }
   }
 }
 
-__device__ __forceinline__ void store_row8(void* base, bool bf16, int64_t at, int n,
+__device__ __forceinline__ void store_row8(void* row, bool bf16, int col, int K, bool whole,
                                            const float (&v)[8]) {
+  char* const to = reinterpret_cast<char*>(row) + (int64_t)col * (bf16 ? 2 : 4);
+  const int n = K - col - (int)row_lane8();
   if (bf16) {
-    uint16_t* p = reinterpret_cast<uint16_t*>(base) + at;
-    if (n >= 8) {
-      uint32_t w[4];
+    char* const p = to + row_lane8() * 2u;
+    uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = f32_to_bf16_bits(v[2 * i]) | (f32_to_bf16_bits(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i)
+      w[i] = f32_to_bf16_bits(v[2 * i]) | (f32_to_bf16_bits(v[2 * i + 1]) << 16);
+    if (whole || n >= 8) {
       __builtin_memcpy(p, w, 16);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = (uint16_t)f32_to_bf16_bits(v[i]);
+        if (i < n) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
     }
   } else {
-    float* p = reinterpret_cast<float*>(base) + at;
-    if (n >= 8) {
+    char* const p = to + row_lane8() * 4u;
+    if (whole || n >= 8) {
       __builtin_memcpy(p, v, 32);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = v[i];
+        if (i < n) reinterpret_cast<float*>(p)[i] = v[i];
     }
   }
 }
@@ -169,50 +196,55 @@ __device__ __forceinline__ void act_row8(int act, float (&g)[8]) {
 // ties to even, decided as the real quotient decides it, not as a rounded
 // one does.
 struct RowCoder {
-  float top, lift, r;
+  float top, r;
   bool bad;          // the row holds an infinity or a NaN: codes 0, scale NaN
+  bool tiny;         // 127 / top might overflow: every code by the quotient
   __device__ __forceinline__ explicit RowCoder(float max_bits) {
+    top = max_bits;
     bad = __float_as_uint(max_bits) >= 0x7F800000u;
-    // 127 / top overflows below 2^-121: such rows are lifted by 2^100 first
-    lift = max_bits < 0x1p-100f ? 0x1p100f : 1.0f;
-    top = max_bits * lift;
-    r = bad || max_bits == 0.0f ? 0.0f : 127.0f / top;
+    tiny = max_bits > 0.0f && max_bits < 0x1p-100f;
+    r = bad || tiny || max_bits == 0.0f ? 0.0f : 127.0f / max_bits;
   }
-  __device__ __forceinline__ float scale(float max_bits) const {
-    return bad ? __uint_as_float(0x7FC00000u) : max_bits / 127.0f;
+  __device__ __forceinline__ float scale(float norm) const {
+    return bad ? __uint_as_float(0x7FC00000u) : top * norm / 127.0f;
   }
-  // v r is within 2 roundings of a value of at most 127, 1.6e-5, of the
-  // quotient: only a product nearer than that to a half is decided by the
-  // quotient itself, in 64 bits (127 v is exact there and a quotient of
-  // floats that is no tie is further than 2^-33 from one).
+  // The codes of 8 values as two dwords. v r + 1.5 2^23 rounds v r to a whole
+  // number, whose low byte is the sum's low byte. r is off by a rounding, so
+  // that the product (at most 127) is off by at most 8e-6 from the quotient:
+  // only one nearer than 3e-5 to a half is decided by the quotient itself, in
+  // 64 bits (127 v is exact there, and a quotient of floats that is no tie is
+  // further than 2^-33 from one).
   __device__ __forceinline__ uint2 codes(const float (&v)[8]) const {
-    float q[8];
-    bool near = false;
+    constexpr float kWhole = 12582912.0f;
+    uint32_t u[8];
+    float far = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float t = v[i] * lift * r;
-      q[i] = rintf(t);
-      near = near || fabsf(t - q[i]) > 0.49997f;
+      const float w = fmaf(v[i], r, kWhole);
+      u[i] = __float_as_uint(w);
+      far = fmaxf(far, fabsf(fmaf(v[i], r, kWhole - w)));
     }
-    if (near) {
+    if (__builtin_amdgcn_ballot_w64(tiny || far > 0.49997f) != 0) {
+      asm volatile("");      // (a branch: computed anyway and selected, it took half of the kernel's time)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        q[i] = (float)rint((double)(v[i] * lift) * 127.0 / (double)top);
+        u[i] = (uint32_t)(int)rint((double)v[i] * 127.0 / (double)top);
     }
-    uint32_t w[2] = {0, 0};
-    if (!bad) {
+    uint32_t o[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i >> 2] |= ((uint32_t)(int)q[i] & 0xFFu) << (8 * (i & 3));
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t lo = __builtin_amdgcn_perm(u[4 * h + 1], u[4 * h], 0x00000400u);
+      const uint32_t hi = __builtin_amdgcn_perm(u[4 * h + 3], u[4 * h + 2], 0x00000400u);
+      o[h] = bad ? 0u : __builtin_amdgcn_perm(hi, lo, 0x05040100u);
     }
-    return make_uint2(w[0], w[1]);
+    return make_uint2(o[0], o[1]);
   }
 };
 
-// One 8-code piece of a row at column s (a multiple of 8) of K: written where
-// it lies below K rounded up to 16, so the row's pad to 16 holds zeros.
-__device__ __forceinline__ void store_codes(int8_t* q, int64_t row_at, int64_t s, int64_t K,
-                                            uint2 w) {
-  if (s < ((K + 15) & ~(int64_t)15)) *reinterpret_cast<uint2*>(q + row_at + s) = w;
+// The codes of the piece at column col of a row: written where they lie below
+// K rounded up to 16, so the row's pad to 16 holds zeros.
+__device__ __forceinline__ void store_codes(int8_t* row, int col, int K, uint2 w) {
+  if (col + (int)row_lane8() < ((K + 15) & ~15)) *reinterpret_cast<uint2*>(row + col + row_lane8()) = w;
 }
 
 }  // namespace lq

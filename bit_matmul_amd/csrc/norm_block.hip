@@ -46,101 +46,133 @@ __device__ __forceinline__ float inv_rms(float (&v)[C][2][8], int K, float eps, 
   return 1.0f / sqrtf(s / (float)K);
 }
 
-template <int C>
-__device__ __forceinline__ void apply_norm(float (&v)[C][2][8], float r, const float* w, bool one_plus,
-                                           int K, int wave, int waves, int lane) {
-#pragma unroll
-  for (int i = 0; i < C; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int s = (wave + i * waves) * kRowBlock + 512 * j + 8 * lane;
-      float g[8];
-      if (w != nullptr) load_row8<false>(w, s, K - s, g);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float wk = w == nullptr ? 1.0f : one_plus ? 1.0f + g[k] : g[k];
-        v[i][j][k] = v[i][j][k] * r * wk;
-      }
-    }
-}
-
-template <int C, bool kYBF16, bool kHBF16>
-__global__ __launch_bounds__(1024) void norm_block_kernel(NormBlock p) {
+// Rows of up to 16K (C = 1) load every tensor before the first reduction and
+// a norm's weights before its own: each reduction waits for the slowest
+// wavefront, and a load behind it would add the memory's latency once more.
+// All of it at the start cost more than it gave: with the registers of both
+// weights fewer workgroups fit (8192 channels, 2048 rows 31 -> 35 us).
+template <int C, bool kYBF16, bool kHBF16, bool kEarly>
+__global__ __launch_bounds__(1024, (C == 1 && !kEarly ? 8 : 4)) void norm_block_kernel(NormBlock p) {
   __shared__ float red[5][kRowMaxWaves];
-  const int wave = wave_id(), lane = threadIdx.x & 63, waves = (int)blockDim.x >> 6;
   const int64_t b = blockIdx.x;
   const int K = (int)p.K;
+  const bool whole = C < 4 && row_whole<C>(K);
   float v[C][2][8];
+  RowPiece<kYBF16> y[2], g[2];
+  RowPiece<kHBF16> h[2];
+  auto row = [&](const void* base, int64_t ld, bool bf16) __attribute__((always_inline)) {
+    return reinterpret_cast<const char*>(base) + b * ld * (bf16 ? 2 : 4);
+  };
+  // the pieces of block i of a row
+  auto load = [&](auto& piece, const void* from, int i) __attribute__((always_inline)) {
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_piece(piece[j], from, row_col(i, j), K, true);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_piece(piece[j], from, row_col(i, j), K, false);
+    }
+  };
+  const char* const yrow = row(p.y, p.ldy, kYBF16);
+  const char* const grow = row(p.gate, p.ldg, kYBF16);
+  const char* const hrow = row(p.h, p.ldh, kHBF16);
+  auto load_weights = [&](RowPiece<false> (&piece)[2], const float* w, int i) __attribute__((always_inline)) {
+    if (w != nullptr) load(piece, w, i);
+  };
+  // fn(values, block, piece) for all of a thread's pieces
   auto each = [&](auto fn) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < C; ++i)
+    for (int i = 0; i < C; ++i) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fn(v[i][j], (wave + i * waves) * kRowBlock + 512 * j + 8 * lane);
+      for (int j = 0; j < 2; ++j) fn(v[i][j], i, j);
+      if constexpr (C == 4) __builtin_amdgcn_sched_barrier(0);   // (one block's loads in registers at a time)
+    }
   };
   auto gate = [&] __attribute__((always_inline)) {
-    each([&](float (&u)[8], int s) __attribute__((always_inline)) {
-      float g[8];
-      load_row8<kYBF16>(p.gate, b * p.ldg + s, K - s, g);
-      act_row8(p.act, g);
+    each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
+      if (!kEarly && j == 0) load(g, grow, i);
+      float a[8];
+      g[j].get(a);
+      act_row8(p.act, a);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] *= g[k];
+      for (int k = 0; k < 8; ++k) u[k] *= a[k];
     });
   };
+  auto norm = [&](float* lds, const float* w) __attribute__((always_inline)) {
+    RowPiece<false> wp[2];
+    if (kEarly) load_weights(wp, w, 0);
+    const float r = inv_rms<C>(v, K, p.eps, lds);
+    const float plus = p.one_plus ? 1.0f : 0.0f;
+    each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
+      if (!kEarly && j == 0) load_weights(wp, w, i);
+      float a[8];
+      wp[j].get(a);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = u[k] * r * (w != nullptr ? plus + a[k] : 1.0f);
+    });
+  };
+  if constexpr (kEarly) {
+    if (p.y != nullptr) load(y, yrow, 0);
+    if (p.gate != nullptr) load(g, grow, 0);
+    if (p.h != nullptr) load(h, hrow, 0);
+  }
   if (p.y != nullptr) {
-    each([&](float (&u)[8], int s) __attribute__((always_inline)) {
-      load_row8<kYBF16>(p.y, b * p.ldy + s, K - s, u);
+    each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
+      if (!kEarly && j == 0) load(y, yrow, i);
+      y[j].get(u);
     });
     if (p.gate != nullptr && p.gate_first) gate();
-    if (p.post)
-      apply_norm<C>(v, inv_rms<C>(v, K, p.eps, red[0]), p.w_post, p.one_plus, K, wave, waves, lane);
+    if (p.post) norm(red[0], p.w_post);
     if (p.gate != nullptr && !p.gate_first) gate();
   }
   if (p.h != nullptr) {
-    each([&](float (&u)[8], int s) __attribute__((always_inline)) {
-      float h[8];
-      load_row8<kHBF16>(p.h, b * p.ldh + s, K - s, h);
+    each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
+      if (!kEarly && j == 0) load(h, hrow, i);
+      float a[8];
+      h[j].get(a);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = p.y != nullptr ? fmaf(p.alpha, u[k], h[k]) : h[k];
+      for (int k = 0; k < 8; ++k) u[k] = p.y != nullptr ? fmaf(p.alpha, u[k], a[k]) : a[k];
     });
   } else {
-    each([&](float (&u)[8], int) __attribute__((always_inline)) {
+    each([&](float (&u)[8], int, int) __attribute__((always_inline)) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) u[k] *= p.alpha;
     });
   }
   if (p.h_out != nullptr)
-    each([&](float (&u)[8], int s) __attribute__((always_inline)) {
-      store_row8(p.h_out, kHBF16, b * p.ldho + s, K - s, u);
+    each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
+      store_row8(const_cast<char*>(row(p.h_out, p.ldho, kHBF16)), kHBF16, row_col(i, j), K, whole, u);
     });
-  if (p.pre)
-    apply_norm<C>(v, inv_rms<C>(v, K, p.eps, red[2]), p.w_pre, p.one_plus, K, wave, waves, lane);
+  if (p.pre) norm(red[2], p.w_pre);
   if (p.a != nullptr)
-    each([&](float (&u)[8], int s) __attribute__((always_inline)) {
-      store_row8(p.a, p.a_bf16, b * p.lda + s, K - s, u);
+    each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
+      store_row8(const_cast<char*>(row(p.a, p.lda, p.a_bf16)), p.a_bf16, row_col(i, j), K, whole, u);
     });
   if (p.q != nullptr) {
     float m = 0.0f;
-    each([&](float (&u)[8], int) __attribute__((always_inline)) {
+    each([&](float (&u)[8], int, int) __attribute__((always_inline)) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) m = MaxBits::of(m, fabsf(u[k]));
     });
     m = row_reduce<MaxBits>(m, red[4]);
     const RowCoder coder(m);
-    each([&](float (&u)[8], int s) __attribute__((always_inline)) {
-      store_codes(p.q, b * p.ldq, s, K, coder.codes(u));
+    each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
+      store_codes(p.q + b * p.ldq, row_col(i, j), K, coder.codes(u));
     });
-    if (threadIdx.x == 0) p.scale[b] = coder.scale(m);
+    if (threadIdx.x == 0) p.scale[b] = coder.scale(1.0f);
   }
 }
 
-template <int C>
+constexpr int64_t kEarlyRows = 256;
+
+template <int C, bool kEarly>
 void enqueue(const NormBlock& p, dim3 grid, dim3 block, hipStream_t stream) {
   if (p.y_bf16) {
-    if (p.h_bf16) hipLaunchKernelGGL((norm_block_kernel<C, true, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((norm_block_kernel<C, true, false>), grid, block, 0, stream, p);
+    if (p.h_bf16) hipLaunchKernelGGL((norm_block_kernel<C, true, true, kEarly>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((norm_block_kernel<C, true, false, kEarly>), grid, block, 0, stream, p);
   } else {
-    if (p.h_bf16) hipLaunchKernelGGL((norm_block_kernel<C, false, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((norm_block_kernel<C, false, false>), grid, block, 0, stream, p);
+    if (p.h_bf16) hipLaunchKernelGGL((norm_block_kernel<C, false, true, kEarly>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((norm_block_kernel<C, false, false, kEarly>), grid, block, 0, stream, p);
   }
 }
 
@@ -150,9 +182,10 @@ hipError_t launch_norm_block(const NormBlock& p, hipStream_t stream) {
   (void)hipGetLastError();   // clear a stale error of an earlier runtime call
   const RowShape s = row_shape(p.K);
   const dim3 grid((unsigned)p.B), block(64u * (unsigned)s.waves);
-  if (s.c == 1) enqueue<1>(p, grid, block, stream);
-  else if (s.c == 2) enqueue<2>(p, grid, block, stream);
-  else enqueue<4>(p, grid, block, stream);
+  if (s.c == 1 && p.B <= kEarlyRows) enqueue<1, true>(p, grid, block, stream);
+  else if (s.c == 1) enqueue<1, false>(p, grid, block, stream);
+  else if (s.c == 2) enqueue<2, false>(p, grid, block, stream);
+  else enqueue<4, false>(p, grid, block, stream);
   return hipGetLastError();
 }
 

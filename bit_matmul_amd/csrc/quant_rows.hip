@@ -6,98 +6,145 @@
 // One workgroup per row, the row in registers (lq_rows.h): it is read once,
 // its maximum is one reduction over the workgroup, and the codes are written
 // from the same registers. The time is that of the bytes.
+#include <type_traits>
+
 #include "lq_rows.h"
 
 namespace lq {
 namespace {
 
-// Stage `bit` of the transform is a butterfly over bit `bit` of the index
-// within the block: bits 0..2 pair the 8 values of a piece, bits 3..8 pair
-// lanes, bit 9 pairs the two pieces.
-__device__ __forceinline__ void fwht_block(float (&v)[2][8], int lhb, int lane) {
+// A butterfly over a lane bit (16 or 32) by exchanging it with register bit
+// kReg: afterwards that register bit is the index bit and the lane bit holds
+// what the register bit held. swap_back undoes it on the codes.
+template <int kLaneBit>
+__device__ __forceinline__ void lane_swap(uint32_t& x, uint32_t& y) {
+  if constexpr (kLaneBit == 16) {
+    const auto z = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    x = z[0];
+    y = z[1];
+  } else {
+    const auto z = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+    x = z[0];
+    y = z[1];
+  }
+}
+template <int kLaneBit, int kReg>
+__device__ __forceinline__ void swap_stage(float (&a)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if ((k & kReg) == 0) {
+      uint32_t x = __float_as_uint(a[k]), y = __float_as_uint(a[k | kReg]);
+      lane_swap<kLaneBit>(x, y);
+      a[k] = __uint_as_float(x) + __uint_as_float(y);
+      a[k | kReg] = __uint_as_float(x) - __uint_as_float(y);
+    }
+}
+template <int kReg>
+__device__ __forceinline__ void reg_stage(float (&a)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if ((k & kReg) == 0) {
+      const float x = a[k], y = a[k | kReg];
+      a[k] = x + y;
+      a[k | kReg] = x - y;
+    }
+}
+
+// The unnormalised Walsh-Hadamard transform of every 2^lhb values of a block.
+// Index bits 0..2 and 9 are register bits, bits 3..8 lane bits; bits 7 and 8
+// end up as register bits 2 and 3 (fwht_order puts the codes back).
+__device__ __forceinline__ void fwht_block(float (&v)[2][8], int lhb) {
+  const int lane = threadIdx.x & 63;
   float a[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) a[k] = v[k >> 3][k & 7];
-#pragma unroll
-  for (int s = 0; s < 3; ++s)
-    if (s < lhb) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if ((k & (1 << s)) == 0) {
-          const float x0 = a[k], x1 = a[k | (1 << s)];
-          a[k] = x0 + x1;
-          a[k | (1 << s)] = x0 - x1;
-        }
-    }
+  reg_stage<1>(a);
+  if (lhb > 1) reg_stage<2>(a);
+  if (lhb > 2) reg_stage<4>(a);
+  if (lhb > 9) reg_stage<8>(a);
   if (lhb > 3) lane_stage<1>(a, lane);
   if (lhb > 4) lane_stage<2>(a, lane);
   if (lhb > 5) lane_stage<4>(a, lane);
   if (lhb > 6) lane_stage<8>(a, lane);
-  if (lhb > 7) lane_stage<16>(a, lane);
-  if (lhb > 8) lane_stage<32>(a, lane);
-  if (lhb > 9) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x0 = a[k], x1 = a[k + 8];
-      a[k] = x0 + x1;
-      a[k + 8] = x0 - x1;
-    }
-  }
+  if (lhb > 7) swap_stage<16, 4>(a);
+  if (lhb > 8) swap_stage<32, 8>(a);
 #pragma unroll
   for (int k = 0; k < 16; ++k) v[k >> 3][k & 7] = a[k];
 }
+// w[j]: the codes of piece j (dword h: register bit 2 set).
+__device__ __forceinline__ void fwht_order(uint2 (&w)[2], int lhb) {
+  if (lhb > 8) {
+    lane_swap<32>(w[0].x, w[1].x);
+    lane_swap<32>(w[0].y, w[1].y);
+  }
+  if (lhb > 7) {
+    lane_swap<16>(w[0].x, w[0].y);
+    lane_swap<16>(w[1].x, w[1].y);
+  }
+}
 
+// Wavefronts on a SIMD: two workgroups' registers have room (gated rows of
+// 28672), so that one loads while the other computes.
 template <int C, bool kXBF16, bool kGate>
-__global__ __launch_bounds__(1024) void quant_rows_kernel(QuantRows p) {
+__global__ __launch_bounds__(1024, (C == 1 ? 8 : C == 2 ? 7 : 4)) void quant_rows_kernel(QuantRows p) {
   __shared__ float red[kRowMaxWaves];
-  const int wave = wave_id(), lane = threadIdx.x & 63, waves = (int)blockDim.x >> 6;
   const int64_t b = blockIdx.x;
+  const int K = (int)p.K;
+  const bool whole = row_whole<C>(K);
+  const char* const xrow = reinterpret_cast<const char*>(p.x) + b * p.ldx * (kXBF16 ? 2 : 4);
+  const char* const grow = reinterpret_cast<const char*>(p.gate) + b * p.ldg * (kXBF16 ? 2 : 4);
   float v[C][2][8];
   float m = 0.0f;
+  // G blocks' loads at a time
+  constexpr int G = C == 4 ? 1 : C;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
+  for (int i0 = 0; i0 < C; i0 += G) {
+    RowPiece<kXBF16> x[G][2], g[G][2];
+    auto load = [&](auto wholec) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int s = (wave + i * waves) * kRowBlock + 512 * j + 8 * lane;
-      load_row8<kXBF16>(p.x, b * p.ldx + s, (int)p.K - s, v[i][j]);
-    }
-  }
-  if constexpr (kGate) {
+      for (int i = 0; i < G; ++i)
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
+        for (int j = 0; j < 2; ++j) {
+          load_piece(x[i][j], xrow, row_col(i0 + i, j), K, decltype(wholec)::value);
+          if constexpr (kGate) load_piece(g[i][j], grow, row_col(i0 + i, j), K, decltype(wholec)::value);
+        }
+    };
+    if (whole) load(std::true_type{});
+    else load(std::false_type{});
+#pragma unroll
+    for (int i = 0; i < G; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int s = (wave + i * waves) * kRowBlock + 512 * j + 8 * lane;
-        float g[8];
-        load_row8<kXBF16>(p.gate, b * p.ldg + s, (int)p.K - s, g);
-        act_row8(p.act, g);
+        x[i][j].get(v[i0 + i][j]);
+        if constexpr (kGate) {
+          float a[8];
+          g[i][j].get(a);
+          act_row8(p.act, a);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][j][k] *= g[k];
+          for (int k = 0; k < 8; ++k) v[i0 + i][j][k] *= a[k];
+        }
       }
-    }
+    if constexpr (C == 4) __builtin_amdgcn_sched_barrier(0);
   }
   if (p.c != nullptr) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
+      RowPiece<false> c[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_piece(c[j], p.c, row_col(i, j), K, whole);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int s = (wave + i * waves) * kRowBlock + 512 * j + 8 * lane;
-        float c[8];
-        load_row8<false>(p.c, s, (int)p.K - s, c);
+        float a[8];
+        c[j].get(a);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][j][k] *= c[k];
+        for (int k = 0; k < 8; ++k) v[i][j][k] *= a[k];
       }
+      if constexpr (C == 4) __builtin_amdgcn_sched_barrier(0);
     }
   }
   if (p.lhb > 0) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      fwht_block(v[i], p.lhb, lane);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][j][k] *= p.norm;
-    }
+    for (int i = 0; i < C; ++i) fwht_block(v[i], p.lhb);
   }
 #pragma unroll
   for (int i = 0; i < C; ++i)
@@ -106,15 +153,17 @@ __global__ __launch_bounds__(1024) void quant_rows_kernel(QuantRows p) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) m = MaxBits::of(m, fabsf(v[i][j][k]));
   m = row_reduce<MaxBits>(m, red);
+  // (the transform's 1 / sqrt(hb) scales v and its maximum alike: the codes
+  // do not see it)
   const RowCoder coder(m);
 #pragma unroll
-  for (int i = 0; i < C; ++i)
+  for (int i = 0; i < C; ++i) {
+    uint2 w[2] = {coder.codes(v[i][0]), coder.codes(v[i][1])};
+    if (p.lhb > 7) fwht_order(w, p.lhb);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int s = (wave + i * waves) * kRowBlock + 512 * j + 8 * lane;
-      store_codes(p.q, b * p.ldq, s, p.K, coder.codes(v[i][j]));
-    }
-  if (threadIdx.x == 0) p.scale[b] = coder.scale(m);
+    for (int j = 0; j < 2; ++j) store_codes(p.q + b * p.ldq, row_col(i, j), K, w[j]);
+  }
+  if (threadIdx.x == 0) p.scale[b] = coder.scale(p.norm);
 }
 
 template <int C>
