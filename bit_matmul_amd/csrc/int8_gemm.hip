@@ -322,17 +322,27 @@ __global__ __launch_bounds__(256) void int8_join_kernel(Int8Gemm p, int tiles_n,
   const int ij = (int)(rest % (PN * PB)), wave = (int)(rest / (PN * PB)) & 3;
   const int t = (int)(rest / (4 * PN * PB));
   if (t >= tiles) return;
-  const int64_t stride = (int64_t)tiles * (4 * PN * PB * 64);
-  const i32x4* in = reinterpret_cast<const i32x4*>(partial) + id;
-  i32x4 v = *in;
-  for (int k = 1; k < ksplit; ++k) v += in[k * stride];
   const TilePlace at = tile_place(t, tiles_n, tiles_b, group_n);
   const int64_t n = (int64_t)at.n * (32 * PN) + 16 * ((wave & 1) * PN + ij / PB) + 4 * (lane >> 4);
   const int64_t b = (int64_t)at.b * (32 * PB) + 16 * ((wave >> 1) * PB + ij % PB) + (lane & 15);
   if (n >= p.N || b >= p.B) return;
+  // (everything is loaded before anything is used: a launch this short is
+  // one trip to memory long)
   float rs[4], bias[4];
   load_int8_rows(p, n, rs, bias);
-  store_int8_sums(p, b, n, p.scale[b], rs, bias, v);
+  const float sb = p.scale[b];
+  const int64_t stride = (int64_t)tiles * (4 * PN * PB * 64);
+  const i32x4* in = reinterpret_cast<const i32x4*>(partial) + id;
+  i32x4 v = {0, 0, 0, 0};
+  for (int k0 = 0; k0 < ksplit; k0 += 8) {
+    i32x4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = in[min(k0 + k, ksplit - 1) * stride];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k0 + k < ksplit) v += x[k];
+  }
+  store_int8_sums(p, b, n, sb, rs, bias, v);
 }
 
 }  // namespace
