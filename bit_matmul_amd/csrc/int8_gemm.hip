@@ -3,24 +3,25 @@
 //
 // A workgroup of 4 wavefronts takes a tile of 32 PN weight rows x 32 PB
 // tokens; wavefront (wn, wb) owns PN panels of 16 rows x PB panels of 16
-// tokens. The reduction runs in steps of 128 bytes (whole cache lines). A
-// step's operands are 4 PN + 4 PB blocks of 1 KB, each 128 bytes of 8 rows,
-// copied straight from memory to LDS (global_load_lds); S stages of LDS hold
-// the step in use and those being copied: S = 2 for the large tiles, whose
-// step is 128 products long, S = 4 for the small ones, which are bound by the
-// memory's latency and need more bytes in flight (8192 x 28672 at 16 tokens:
-// 51 -> 45 us against 64-byte steps).
+// tokens. The reduction runs in steps of KB bytes, whole cache lines: 128 for
+// the large tiles, 256 for the small ones, whose time is that of the weights'
+// stream and grows shorter with the runs that a row is read in (27648 x 5120
+// at 64 tokens 39 -> 36 us; 64-byte steps took 51 us at 8192 x 28672, 16
+// tokens, where 128 and 256 take 47 and 46). A step's operands are blocks of
+// 1 KB, copied straight from memory to LDS (global_load_lds); S stages of LDS
+// hold the step in use and those being copied: as many as leave room for the
+// workgroups that share a compute unit.
 //
-// Row r of a panel (blocks of 8 rows in pairs) keeps its 16-byte chunk c at
-// 128 r + 16 (c ^ f(r)), f(r) = (r & 7) ^ (r >> 3): any 8 lanes of consecutive
-// rows that read the same chunk then touch 32 different banks, any 16 touch
-// 64. The copy of a block puts lane l's 16 bytes at 16 l, so lane l reads
-// chunk (l & 7) ^ f of row l >> 3: eight lanes read a whole line.
+// Row r of a panel keeps its 16-byte chunk c at KB r + 16 (c ^ f(r)), f(r) =
+// (r & 7) ^ (r >> 3) for 8 chunks, r for 16: any 8 lanes of consecutive rows
+// that read the same chunk then touch 32 different banks, any 16 touch 64.
+// The copy of a block puts lane l's 16 bytes at 16 l, so lanes in turn read
+// the chunks of one row in the order that f gives: whole lines.
 //
-// One barrier per step, before its second half: passing it, a wavefront knows
+// One barrier per step, before its last 64 bytes: passing it, a wavefront knows
 // that the next step's stage is full (each waited for its own copies) and
 // that this step's has been read into registers by all, so its space takes
-// the copies of step s + S. Operands are read one half ahead, between the
+// the copies of step s + S. Operands are read 64 bytes ahead, between the
 // products, and the copies are spread among the products: bunched up, they
 // filled the load unit's queue while the matrix cores waited (8192 x 28672 at
 // 2048 tokens 489 -> 404 us). There, 380 to 405 us (2.4 to 2.5 POP/s) of
@@ -68,16 +69,18 @@ __device__ __forceinline__ void mfma_zero(i32x4& acc) {
 }
 __device__ __forceinline__ void acc_ready() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
-template <int PN, int PB, int S>
+template <int PN, int PB, int S, int KB>
 __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
     Int8Gemm p, int tiles_n, int tiles_b, int group_n, int ksplit, int* partial) {
-  static_assert(S == 2 || S == 4, "stages");
-  constexpr int kBlocks = 4 * PN + 4 * PB;     // 8 rows x 128 bytes each
-  constexpr int kCopies = PN + PB;             // per wavefront and step
+  static_assert(S >= 2 && S <= 4 && (KB == 128 || KB == 256), "stages");
+  constexpr int kChunks = KB / 16;             // 16-byte chunks of a row in a step
+  constexpr int kCopies = (PN + PB) * KB / 128;   // per wavefront and step, 1 KB each
+  constexpr int kBlocks = 4 * kCopies;
+  constexpr int kW = PN * KB / 128;            // of a wavefront's copies, those of weights
   __shared__ uint4 stage0[kBlocks * 64];
   __shared__ uint4 stage1[kBlocks * 64];
   __shared__ uint4 stage2[S > 2 ? kBlocks * 64 : 1];
-  __shared__ uint4 stage3[S > 2 ? kBlocks * 64 : 1];
+  __shared__ uint4 stage3[S > 3 ? kBlocks * 64 : 1];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int g = lane >> 4, r = lane & 15;
   const int wn = wave & 1, wb = wave >> 1;
@@ -97,16 +100,17 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
   const int64_t b0 = (int64_t)__builtin_amdgcn_readfirstlane(place.b) * (32 * PB);
 
   const int K16 = ((int)p.K + 15) & ~15;
-  const int all = (K16 + 127) / 128, full = K16 / 128;
+  const int all = (K16 + KB - 1) / KB, full = K16 / KB;
   // This workgroup's steps: s0 .. steps - 1.
   const int s0 = (int)((int64_t)all * part_k / ksplit), steps = (int)((int64_t)all * (part_k + 1) / ksplit);
 
-  // Copy k of this wavefront: block wave + 4 k, this lane's row and chunk of
-  // it. Chunks past K (in the last step) are read as the row's first one, and
-  // the codes that came that way are then zeroed in LDS by the lanes that
-  // copied them.
-  const int row = lane >> 3;
-  const int chunk = (lane & 7) ^ row ^ (wave & 1);
+  // Copy k of this wavefront: block wave + 4 k, of 64 / kChunks rows; this
+  // lane's row and chunk of it. Chunks past K (in the last step) are read as
+  // the row's first one, and the codes that came that way are then zeroed in
+  // LDS by the lanes that copied them.
+  const int row = lane / kChunks;
+  const int panel_row = (wave * (64 / kChunks) + row) & 15;
+  const int chunk = (lane % kChunks) ^ (KB == 128 ? (panel_row & 7) ^ (panel_row >> 3) : panel_row);
   const int rows_n = (int)min((int64_t)(32 * PN), p.N - n0);
   const int rows_b = (int)min((int64_t)(32 * PB), p.B - b0);
   const int8_t* const wbase = p.w + n0 * p.ldw;
@@ -114,16 +118,16 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
   uint32_t off[kCopies];
 #pragma unroll
   for (int k = 0; k < kCopies; ++k) {
-    const int rr = 8 * (wave + 4 * (k < PN ? k : k - PN)) + row;
-    off[k] = k < PN ? (uint32_t)min(rr, rows_n - 1) * (uint32_t)p.ldw
+    const int rr = (64 / kChunks) * (wave + 4 * (k < kW ? k : k - kW)) + row;
+    off[k] = k < kW ? (uint32_t)min(rr, rows_n - 1) * (uint32_t)p.ldw
                     : (uint32_t)min(rr, rows_b - 1) * (uint32_t)p.ldq;
   }
   auto lane_at = [&](int s) __attribute__((always_inline)) {
-    const uint32_t at = 128u * (uint32_t)min(s, steps - 1) + 16u * (uint32_t)chunk;
+    const uint32_t at = (uint32_t)KB * (uint32_t)min(s, steps - 1) + 16u * (uint32_t)chunk;
     return at < (uint32_t)K16 ? at : 0u;
   };
   auto copy_one = [&](int k, uint32_t at, uint4* dst) __attribute__((always_inline)) {
-    __builtin_amdgcn_global_load_lds((const void*)((k < PN ? wbase : qbase) + (off[k] + at)),
+    __builtin_amdgcn_global_load_lds((const void*)((k < kW ? wbase : qbase) + (off[k] + at)),
                                      (__attribute__((address_space(3))) void*)(dst + (wave + 4 * k) * 64), 16,
                                      0, 0);
   };
@@ -132,18 +136,20 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
 #pragma unroll
     for (int k = 0; k < kCopies; ++k) copy_one(k, at, dst);
   };
-  // The step that ends inside its 128 bytes, if one of this workgroup's does.
+  // The step that ends inside its KB bytes, if one of this workgroup's does.
   const int part = full < steps && full < all ? full : -1;
   auto zero_past = [&](uint4* st) __attribute__((always_inline)) {
-    if (128 * full + 16 * chunk < K16) return;
+    if (KB * full + 16 * chunk < K16) return;
 #pragma unroll
-    for (int k = PN; k < kCopies; ++k) st[(wave + 4 * k) * 64 + lane] = make_uint4(0, 0, 0, 0);
+    for (int k = kW; k < kCopies; ++k) st[(wave + 4 * k) * 64 + lane] = make_uint4(0, 0, 0, 0);
   };
-  // Units of 16 bytes: row r's chunk g of half h lies at 8 r + (4 h + g ^ f(r)).
-  const int rd = 8 * r + (g ^ (r & 7) ^ (r >> 3));
-  const int rd_a = wn * PN * 128, rd_c = (2 * PN + wb * PB) * 128;
+  // Units of 16 bytes: row r's chunk 4 h + g (part h of the step, 64 bytes)
+  // lies at kChunks r + ((4 h + g) ^ f(r)).
+  const int rd = kChunks * r + (g ^ (KB == 128 ? (r & 7) ^ (r >> 3) : r));
+  auto rd_part = [&](int h) __attribute__((always_inline)) { return rd ^ (4 * h); };
+  const int rd_a = wn * PN * KB, rd_c = (2 * PN + wb * PB) * KB;
   auto stage_c = [&](auto ic) __attribute__((always_inline)) -> uint4* {
-    constexpr int i = decltype(ic)::value & (S - 1);
+    constexpr int i = decltype(ic)::value % S;
     if constexpr (i == 0) return stage0;
     else if constexpr (i == 1) return stage1;
     else if constexpr (i == 2) return stage2;
@@ -164,27 +170,25 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
 
   copy_step(s0, stage0);
   copy_step(s0 + 1, stage1);
-  if constexpr (S > 2) {
-    copy_step(s0 + 2, stage2);
-    copy_step(s0 + 3, stage3);
-  }
+  if constexpr (S > 2) copy_step(s0 + 2, stage2);
+  if constexpr (S > 3) copy_step(s0 + 3, stage3);
   i32x4 a0[PN], c0[PB], a1[PN], c1[PB];
   __builtin_amdgcn_s_waitcnt(kWaitVm0);
   if (part == s0) zero_past(stage0);
   __builtin_amdgcn_s_waitcnt(kWaitLds0);
   __builtin_amdgcn_s_barrier();
 #pragma unroll
-  for (int i = 0; i < PN; ++i) a0[i] = *reinterpret_cast<const i32x4*>(stage0 + rd_a + rd + 128 * i);
+  for (int i = 0; i < PN; ++i) a0[i] = *reinterpret_cast<const i32x4*>(stage0 + rd_a + rd + KB * i);
 #pragma unroll
-  for (int j = 0; j < PB; ++j) c0[j] = *reinterpret_cast<const i32x4*>(stage0 + rd_c + rd + 128 * j);
+  for (int j = 0; j < PB; ++j) c0[j] = *reinterpret_cast<const i32x4*>(stage0 + rd_c + rd + KB * j);
 
-  // Half a step: PN groups of PB products. Each group also issues its share
-  // of the reads of the next half's operands (from `next` at rdn), which the
-  // last groups need not, and with kFill its share of the copies of step
+  // A part of a step: PN groups of PB products. Each group also issues its
+  // share of the reads of the next part's operands (from `next` at rdn), which
+  // the last groups need not, and with kFill its share of the copies of step
   // s + S into the stage of step s. Spread like this, they never queue up
   // before the products.
-  auto half = [&](auto fillc, uint32_t at, uint4* fill, const uint4* next, int rdn, i32x4 (&a)[PN],
-                  i32x4 (&c)[PB], i32x4 (&an)[PN], i32x4 (&cn)[PB]) __attribute__((always_inline)) {
+  auto part_step = [&](auto fillc, uint32_t at, uint4* fill, const uint4* next, int rdn, i32x4 (&a)[PN],
+                       i32x4 (&c)[PB], i32x4 (&an)[PN], i32x4 (&cn)[PB]) __attribute__((always_inline)) {
     constexpr bool kFill = decltype(fillc)::value;
     constexpr int kEarly = PN > 2 ? PN - 2 : 1;                 // groups that read: done two early
     constexpr int kReads = (PN + PB + kEarly - 1) / kEarly;     // operands per such group
@@ -192,8 +196,8 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
     for (int i = 0; i < PN; ++i) {
 #pragma unroll
       for (int x = i * kReads; x < (i + 1) * kReads; ++x) {
-        if (x < PB) cn[x] = *reinterpret_cast<const i32x4*>(next + rd_c + rdn + 128 * x);
-        else if (x < PB + PN) an[x - PB] = *reinterpret_cast<const i32x4*>(next + rd_a + rdn + 128 * (x - PB));
+        if (x < PB) cn[x] = *reinterpret_cast<const i32x4*>(next + rd_c + rdn + KB * x);
+        else if (x < PB + PN) an[x - PB] = *reinterpret_cast<const i32x4*>(next + rd_a + rdn + KB * (x - PB));
       }
 #pragma unroll
       for (int j = 0; j < PB; ++j) {
@@ -208,21 +212,29 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
       }
     }
   };
-  // One step of 128 bytes. Its first half's operands are in a0, c0. Before
-  // the second half reads the next step's stage, that stage is full (every
-  // wavefront waits for its own copies), and this step's has been read into
-  // registers by all and takes the copies of step s + S.
+  // One step of KB bytes in parts of 64. Its first part's operands are in a0,
+  // c0. Before the last part reads the next step's stage, that stage is full
+  // (every wavefront waits for its own copies), and this step's has been read
+  // into registers by all and takes the copies of step s + S.
   auto do_step = [&](auto sc, int s) __attribute__((always_inline)) {
     constexpr int su = decltype(sc)::value;
+    constexpr int kParts = KB / 64;
     uint4* const cur = stage_c(std::integral_constant<int, su>{});
     uint4* const next = stage_c(std::integral_constant<int, su + 1>{});
+#pragma unroll
+    for (int h = 0; h + 2 < kParts; h += 2) {
+      __builtin_amdgcn_s_waitcnt(kWaitLds0);
+      part_step(std::false_type{}, 0u, cur, cur, rd_part(h + 1), a0, c0, a1, c1);
+      __builtin_amdgcn_s_waitcnt(kWaitLds0);
+      part_step(std::false_type{}, 0u, cur, cur, rd_part(h + 2), a1, c1, a0, c0);
+    }
     __builtin_amdgcn_s_waitcnt(kWaitLds0);
-    half(std::false_type{}, 0u, cur, cur, rd ^ 4, a0, c0, a1, c1);
+    part_step(std::false_type{}, 0u, cur, cur, rd_part(kParts - 1), a0, c0, a1, c1);
     __builtin_amdgcn_s_waitcnt(kWaitVm);
     if (s + 1 == part) zero_past(next);
     __builtin_amdgcn_s_waitcnt(kWaitLds0);
     __builtin_amdgcn_s_barrier();
-    half(std::true_type{}, lane_at(s + S), cur, next, rd, a1, c1, a0, c0);
+    part_step(std::true_type{}, lane_at(s + S), cur, next, rd, a1, c1, a0, c0);
   };
   for (int s = s0;;) {
     do_step(std::integral_constant<int, 0>{}, s);
@@ -232,6 +244,8 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
     if constexpr (S > 2) {
       do_step(std::integral_constant<int, 2>{}, s);
       if (++s == steps) break;
+    }
+    if constexpr (S > 3) {
       do_step(std::integral_constant<int, 3>{}, s);
       if (++s == steps) break;
     }
@@ -347,45 +361,48 @@ __global__ __launch_bounds__(256) void int8_join_kernel(Int8Gemm p, int tiles_n,
 
 }  // namespace
 
-template <int PN, int PB, int S>
+template <int PN, int PB, int S, int KB>
 static void enqueue_tile(const Int8Gemm& p, const Int8Plan& plan, int* partial, hipStream_t stream) {
   const int tn = (int)((p.N + 32 * PN - 1) / (32 * PN)), tb = (int)((p.B + 32 * PB - 1) / (32 * PB));
   const int group_n = 4;
   const int per = (tn * tb * plan.ksplit + 7) / 8;
-  hipLaunchKernelGGL((int8_tile_kernel<PN, PB, S>), dim3((unsigned)(8 * per)), dim3(256), 0, stream, p, tn,
+  hipLaunchKernelGGL((int8_tile_kernel<PN, PB, S, KB>), dim3((unsigned)(8 * per)), dim3(256), 0, stream, p, tn,
                      tb, group_n, plan.ksplit, partial);
   if (plan.ksplit > 1)
     hipLaunchKernelGGL((int8_join_kernel<PN, PB>), dim3((unsigned)(tn * tb * PN * PB)), dim3(256), 0,
                        stream, p, tn, tb, group_n, plan.ksplit, partial);
 }
 
-// The tiles, and what they cost in us, fitted to 1420 measurements over 42
-// sizes (1 to 2048 tokens, 100 to 28672 outputs, 200 to 28672 inputs): a step
-// of 128 bytes takes `step` plus `share` for every workgroup on the compute
-// unit, a workgroup's begin and end take `ends`. The choice it gives is on
-// average 2.5% above the best of these tiles and splits.
+// The tiles (stages and bytes per step at the launches below), and what they
+// cost in us, fitted to 1100 measurements over 47 sizes (1 to 2048 tokens, 60
+// to 28672 outputs, 150 to 28672 inputs): a step takes `step` plus `share` for
+// every workgroup on the compute unit, a workgroup's begin and end take
+// `ends`. The choice it gives is on average 1.7% above the best of these
+// tiles and splits, 10% at most. Left out, with what their absence costs on
+// average: 32 x 64 tokens (0%), a 2-stage 32 x 32 (0.1%).
 struct TileCost {
-  int pn, pb, per_cu;
+  int pn, pb, bytes, per_cu;
   float step, share, ends;
 };
 static constexpr TileCost kTiles[] = {
-    {8, 8, 1, 1.38f, 0.0f, 2.8f},  {7, 8, 1, 1.26f, 0.0f, 2.6f}, {6, 8, 1, 1.18f, 0.0f, 2.9f},
-    {4, 8, 1, 1.03f, 0.0f, 3.0f},  {4, 4, 1, 0.60f, 0.0f, 2.6f}, {2, 4, 1, 0.44f, 0.0f, 2.1f},
-    {2, 2, 2, 0.22f, 0.12f, 2.4f}, {2, 1, 3, 0.22f, 0.085f, 2.1f},
+    {8, 8, 128, 1, 1.155f, 0.167f, 3.9f}, {7, 8, 128, 1, 0.932f, 0.262f, 3.1f},
+    {6, 8, 128, 1, 0.774f, 0.372f, 2.9f}, {4, 8, 128, 1, 0.925f, 0.033f, 2.8f},
+    {4, 4, 128, 1, 0.510f, 0.056f, 2.4f}, {4, 2, 256, 1, 0.803f, 0.016f, 1.6f},
+    {2, 4, 256, 1, 0.657f, 0.133f, 1.7f}, {2, 2, 256, 2, 0.532f, 0.202f, 1.4f},
+    {2, 1, 256, 3, 0.477f, 0.189f, 0.8f}, {1, 1, 256, 2, 0.180f, 0.168f, 1.1f},
 };
-constexpr float kJoinUs = 2.5f, kJoinBytesPerUs = 4.0e6f, kStreamBytesPerUs = 5.3e6f;
+constexpr float kJoinUs = 3.5f, kJoinBytesPerUs = 4.0e6f, kStreamBytesPerUs = 6.3e6f;
 constexpr int kMaxSplit = 16;
 constexpr int64_t kMaxTiles = 1 << 22;    // (a launch has fewer than 2^32 threads)
 
 Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus) {
   if (cus <= 0) cus = 256;
-  const int64_t steps = (((K + 15) & ~(int64_t)15) + 127) / 128;
   const float stream = (float)N * (float)K / kStreamBytesPerUs;      // the weights' stream
   Int8Plan best{};
   float best_us = 0.0f;
   for (const TileCost& c : kTiles) {
     const int64_t tiles = ((N + 32 * c.pn - 1) / (32 * c.pn)) * ((B + 32 * c.pb - 1) / (32 * c.pb));
-    const int64_t slots = (int64_t)cus * c.per_cu;
+    const int64_t slots = (int64_t)cus * c.per_cu, steps = (K + c.bytes - 1) / c.bytes;
     if (tiles > kMaxTiles && &c != kTiles) continue;
     for (int ks = 1; ks <= kMaxSplit && ks <= steps; ++ks) {
       if (ks > 1 && tiles * ks > 4 * (int64_t)cus) break;
@@ -396,7 +413,7 @@ Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus) {
         const float load = 0.5f * ((float)rem / cus + (float)((rem + cus - 1) / cus));
         us += len * (c.step + c.share * load) + c.ends;
       }
-      us = us > stream ? us + 0.25f * stream : stream + 0.25f * us;
+      us = us > stream ? us + 0.3f * stream : stream + 0.3f * us;
       const size_t partial = ks > 1 ? (size_t)units * c.pn * c.pb * 4096 : 0;
       if (ks > 1) us += kJoinUs + 2.0f * (float)partial / kJoinBytesPerUs;
       if (best.pn == 0 || us < best_us) {
@@ -411,14 +428,16 @@ Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus) {
 hipError_t launch_int8_gemm(const Int8Gemm& p, const Int8Plan& plan, int* partial, hipStream_t stream) {
   (void)hipGetLastError();   // clear a stale error of an earlier runtime call
   switch (plan.pn * 16 + plan.pb) {
-    case 0x88: enqueue_tile<8, 8, 2>(p, plan, partial, stream); break;
-    case 0x78: enqueue_tile<7, 8, 2>(p, plan, partial, stream); break;
-    case 0x68: enqueue_tile<6, 8, 2>(p, plan, partial, stream); break;
-    case 0x48: enqueue_tile<4, 8, 2>(p, plan, partial, stream); break;
-    case 0x44: enqueue_tile<4, 4, 4>(p, plan, partial, stream); break;
-    case 0x24: enqueue_tile<2, 4, 4>(p, plan, partial, stream); break;
-    case 0x22: enqueue_tile<2, 2, 4>(p, plan, partial, stream); break;
-    case 0x21: enqueue_tile<2, 1, 4>(p, plan, partial, stream); break;
+    case 0x88: enqueue_tile<8, 8, 2, 128>(p, plan, partial, stream); break;
+    case 0x78: enqueue_tile<7, 8, 2, 128>(p, plan, partial, stream); break;
+    case 0x68: enqueue_tile<6, 8, 2, 128>(p, plan, partial, stream); break;
+    case 0x48: enqueue_tile<4, 8, 2, 128>(p, plan, partial, stream); break;
+    case 0x44: enqueue_tile<4, 4, 4, 128>(p, plan, partial, stream); break;
+    case 0x42: enqueue_tile<4, 2, 3, 256>(p, plan, partial, stream); break;
+    case 0x24: enqueue_tile<2, 4, 3, 256>(p, plan, partial, stream); break;
+    case 0x22: enqueue_tile<2, 2, 2, 256>(p, plan, partial, stream); break;
+    case 0x21: enqueue_tile<2, 1, 2, 256>(p, plan, partial, stream); break;
+    case 0x11: enqueue_tile<1, 1, 4, 256>(p, plan, partial, stream); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();

@@ -319,12 +319,13 @@ def test_int8_gemm_largest_sum(lq, B):
 
 # (B, N, K, rows and tokens of the tile, whether the reduction is split)
 VARIANTS = [
-    (3, 1000, 700, 64, 32, False), (1, 500, 3001, 64, 32, True), (129, 10001, 48, 64, 64, False),
-    (1500, 16, 12001, 64, 64, True), (65, 14000, 48, 64, 128, False), (1100, 100, 12001, 64, 128, True),
-    (129, 14000, 48, 128, 128, False), (65, 6000, 12001, 128, 128, True), (257, 14000, 300, 128, 256, False),
-    (400, 5000, 12001, 128, 256, True), (513, 14000, 700, 192, 256, False), (513, 4000, 12001, 192, 256, True),
-    (257, 14000, 48, 224, 256, False), (257, 14000, 12001, 224, 256, True), (1500, 10001, 48, 256, 256, False),
-    (400, 10001, 12001, 256, 256, True),
+    (3, 16, 700, 32, 32, False), (1, 17, 6000, 32, 32, True), (1, 2000, 49, 64, 32, False),
+    (1, 6000, 12001, 64, 32, True), (129, 10001, 48, 64, 64, False), (33, 2000, 12001, 64, 64, True),
+    (100, 14000, 700, 64, 128, False), (1100, 100, 12001, 64, 128, True), (129, 10001, 300, 128, 64, False),
+    (33, 3001, 12001, 128, 64, True), (129, 14000, 48, 128, 128, False), (65, 6000, 12001, 128, 128, True),
+    (257, 14000, 48, 128, 256, False), (400, 5000, 12001, 128, 256, True), (513, 14000, 48, 192, 256, False),
+    (400, 10001, 12001, 192, 256, True), (1100, 10001, 48, 224, 256, False), (257, 14000, 12001, 224, 256, True),
+    (1500, 10001, 48, 256, 256, False), (1100, 4000, 14336, 256, 256, True),
 ]
 
 
