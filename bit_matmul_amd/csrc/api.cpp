@@ -1149,9 +1149,12 @@ lq_status lq_int8_linear(const lq_int8_layer* layer, const void* x, lq_dtype xty
   lq::QuantRows p{x, nullptr, layer->c, q, scale, B, layer->K, ldx, 0, w.ldq, LQ_ACT_NONE, 0, 1.0f,
                   xtype == LQ_BF16};
   fill_hb(&p, layer->hb);
+  const lq::Int8Gemm gemm = gemm_args(layer, q, w.ldq, scale, B, y, ytype, ldy);
+  if (lq::int8_token_applies(p, w.plan))
+    return hip_status(lq::launch_int8_token(p, gemm, (hipStream_t)stream));
   s = hip_status(lq::launch_quant_rows(p, (hipStream_t)stream));
   if (s != LQ_OK) return s;
-  return hip_status(lq::launch_int8_gemm(gemm_args(layer, q, w.ldq, scale, B, y, ytype, ldy), w.plan,
+  return hip_status(lq::launch_int8_gemm(gemm, w.plan,
                                          int8_partial(w.plan, ws, w.off_partial),
                                          (hipStream_t)stream));
 }

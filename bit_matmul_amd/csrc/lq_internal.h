@@ -526,5 +526,8 @@ struct Int8Plan {
 Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus);
 // partial: Int8Plan::partial_bytes of workspace (unused when ksplit is 1).
 hipError_t launch_int8_gemm(const Int8Gemm& p, const Int8Plan& plan, int* partial, hipStream_t stream);
+// Rows and product of one token in one launch (t.q, t.scale and p.q, p.scale unused).
+bool int8_token_applies(const QuantRows& t, const Int8Plan& plan);
+hipError_t launch_int8_token(const QuantRows& t, const Int8Gemm& p, hipStream_t stream);
 
 }  // namespace lq

@@ -191,6 +191,77 @@ __device__ __forceinline__ void act_row8(int act, float (&g)[8]) {
   }
 }
 
+// ------------------------------------------------------------ T
+// A butterfly over a lane bit (16 or 32) by exchanging it with register bit
+// kReg: afterwards that register bit is the index bit and the lane bit holds
+// what the register bit held. swap_back undoes it on the codes.
+template <int kLaneBit>
+__device__ __forceinline__ void lane_swap(uint32_t& x, uint32_t& y) {
+  if constexpr (kLaneBit == 16) {
+    const auto z = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    x = z[0];
+    y = z[1];
+  } else {
+    const auto z = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+    x = z[0];
+    y = z[1];
+  }
+}
+template <int kLaneBit, int kReg>
+__device__ __forceinline__ void swap_stage(float (&a)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if ((k & kReg) == 0) {
+      uint32_t x = __float_as_uint(a[k]), y = __float_as_uint(a[k | kReg]);
+      lane_swap<kLaneBit>(x, y);
+      a[k] = __uint_as_float(x) + __uint_as_float(y);
+      a[k | kReg] = __uint_as_float(x) - __uint_as_float(y);
+    }
+}
+template <int kReg>
+__device__ __forceinline__ void reg_stage(float (&a)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if ((k & kReg) == 0) {
+      const float x = a[k], y = a[k | kReg];
+      a[k] = x + y;
+      a[k | kReg] = x - y;
+    }
+}
+
+// The unnormalised Walsh-Hadamard transform of every 2^lhb values of a block.
+// Index bits 0..2 and 9 are register bits, bits 3..8 lane bits; bits 7 and 8
+// end up as register bits 2 and 3 (fwht_order puts the codes back).
+__device__ __forceinline__ void fwht_block(float (&v)[2][8], int lhb) {
+  const int lane = threadIdx.x & 63;
+  float a[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) a[k] = v[k >> 3][k & 7];
+  reg_stage<1>(a);
+  if (lhb > 1) reg_stage<2>(a);
+  if (lhb > 2) reg_stage<4>(a);
+  if (lhb > 9) reg_stage<8>(a);
+  if (lhb > 3) lane_stage<1>(a, lane);
+  if (lhb > 4) lane_stage<2>(a, lane);
+  if (lhb > 5) lane_stage<4>(a, lane);
+  if (lhb > 6) lane_stage<8>(a, lane);
+  if (lhb > 7) swap_stage<16, 4>(a);
+  if (lhb > 8) swap_stage<32, 8>(a);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k >> 3][k & 7] = a[k];
+}
+// w[j]: the codes of piece j (dword h: register bit 2 set).
+__device__ __forceinline__ void fwht_order(uint2 (&w)[2], int lhb) {
+  if (lhb > 8) {
+    lane_swap<32>(w[0].x, w[1].x);
+    lane_swap<32>(w[0].y, w[1].y);
+  }
+  if (lhb > 7) {
+    lane_swap<16>(w[0].x, w[0].y);
+    lane_swap<16>(w[1].x, w[1].y);
+  }
+}
+
 // ------------------------------------------------------------ 8-bit codes
 // The codes of a row: q = v 127 / top rounded to the nearest whole number,
 // ties to even, decided as the real quotient decides it, not as a rounded

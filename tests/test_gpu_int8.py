@@ -433,6 +433,45 @@ def test_int8_linear_with_the_transform(lq, B):
     assert np.linalg.norm(host64(y) - want) / np.linalg.norm(want) < 0.05
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N,K,hb", [(1, 1, 1), (33, 15, 1), (31, 257, 1), (500, 1000, 1), (32, 1024, 1024),
+                                    (700, 4096, 128), (90, 4097, 1), (8200, 8192, 1024), (9001, 5121, 1),
+                                    (8225, 9216, 512), (8192, 16384, 1), (8193, 16385, 1), (10000, 16384, 64)])
+def test_int8_linear_one_token(lq, N, K, hb, dtype):
+    """One token: the bits of lq_quant_rows and lq_int8_gemm one after another, whichever path it takes."""
+    rng = np.random.default_rng(N + K)
+    c = randn(rng, K).abs() + 0.5 if hb > 1 else None
+    layer, keep = make_layer(lq, rng, N, K, bias=True, hb=hb, c=c)
+    x = randn(rng, 1, K + 1).to(dtype)[:, 1:]
+    out = torch.full((3, N), 9.0, device=DEV)
+    note(f"lq_int8_linear B=1 N={N} K={K} hb={hb} x={dtype}")
+    lq.lq_int8_linear(layer, x, 1, out[1:2], garbage(lq.lq_int8_linear_workspace_size(layer, 1, dtype)))
+    torch.cuda.synchronize()
+    assert torch.all(out[0] == 9.0) and torch.all(out[2] == 9.0)
+    q = torch.empty(1, pad16(K), dtype=torch.int8, device=DEV)[:, :K]
+    s, y = torch.empty(1, device=DEV), torch.empty(1, N, device=DEV)
+    lq.lq_quant_rows(x, 1, K, q, s, hb=hb, c=c)
+    lq.lq_int8_gemm(layer, q, s, 1, y, garbage(lq.lq_int8_gemm_workspace_size(layer, 1)))
+    torch.cuda.synchronize()
+    assert torch.equal(out[1:2], y)
+
+
+def test_int8_linear_one_token_non_finite(lq):
+    rng = np.random.default_rng(9)
+    layer, keep = make_layer(lq, rng, 100, 600)
+    for bad in (float("nan"), float("inf")):
+        x = randn(rng, 1, 600)
+        x[0, 599] = bad
+        y = torch.zeros(1, 100, device=DEV)
+        lq.lq_int8_linear(layer, x, 1, y, garbage(lq.lq_int8_linear_workspace_size(layer, 1, F32)))
+        torch.cuda.synchronize()
+        assert torch.isnan(y).all()
+    lq.lq_int8_linear(layer, torch.zeros(1, 600, device=DEV), 1, y,
+                      garbage(lq.lq_int8_linear_workspace_size(layer, 1, F32)))
+    torch.cuda.synchronize()
+    assert torch.all(y == 0)
+
+
 def test_int8_linear_is_the_transformed_layer(lq):
     """Weights W T^-1 after T give W x: T is orthonormal with unit scales, and its own inverse."""
     rng = np.random.default_rng(6)
