@@ -192,6 +192,28 @@ __device__ __forceinline__ void act_row8(int act, float (&g)[8]) {
 }
 
 // ------------------------------------------------------------ T
+// A butterfly with lane ^ X (1, 2, 4, 8): a + p in the lane whose bit is clear,
+// p - a in the other, as one fma with a multiplier of +-1. (With bound_ctrl
+// the exchange needs no register cleared before it.)
+template <int kDpp>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kDpp, 0xF, 0xF, true));
+}
+template <int X>
+__device__ __forceinline__ void dpp_stage(float (&a)[16], int lane) {
+  const float sgn = (lane & X) != 0 ? -1.0f : 1.0f;
+  float p[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    if constexpr (X == 1) p[k] = dpp<0xB1>(a[k]);                // quad permutations
+    else if constexpr (X == 2) p[k] = dpp<0x4E>(a[k]);
+    else if constexpr (X == 4) p[k] = dpp<0x1B>(dpp<0x141>(a[k]));   // lane ^ 7, then ^ 3
+    else p[k] = dpp<0x128>(a[k]);                                // 16 lanes rotated by 8
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) a[k] = fmaf(a[k], sgn, p[k]);
+}
+
 // A butterfly over a lane bit (16 or 32) by exchanging it with register bit
 // kReg: afterwards that register bit is the index bit and the lane bit holds
 // what the register bit held. swap_back undoes it on the codes.
@@ -232,7 +254,7 @@ __device__ __forceinline__ void reg_stage(float (&a)[16]) {
 // The unnormalised Walsh-Hadamard transform of every 2^lhb values of a block.
 // Index bits 0..2 and 9 are register bits, bits 3..8 lane bits; bits 7 and 8
 // end up as register bits 2 and 3 (fwht_order puts the codes back).
-__device__ __forceinline__ void fwht_block(float (&v)[2][8], int lhb) {
+__device__ __forceinline__ void fwht_stages(float (&v)[2][8], int lhb) {
   const int lane = threadIdx.x & 63;
   float a[16];
 #pragma unroll
@@ -241,14 +263,20 @@ __device__ __forceinline__ void fwht_block(float (&v)[2][8], int lhb) {
   if (lhb > 1) reg_stage<2>(a);
   if (lhb > 2) reg_stage<4>(a);
   if (lhb > 9) reg_stage<8>(a);
-  if (lhb > 3) lane_stage<1>(a, lane);
-  if (lhb > 4) lane_stage<2>(a, lane);
-  if (lhb > 5) lane_stage<4>(a, lane);
-  if (lhb > 6) lane_stage<8>(a, lane);
+  if (lhb > 3) dpp_stage<1>(a, lane);
+  if (lhb > 4) dpp_stage<2>(a, lane);
+  if (lhb > 5) dpp_stage<4>(a, lane);
+  if (lhb > 6) dpp_stage<8>(a, lane);
   if (lhb > 7) swap_stage<16, 4>(a);
   if (lhb > 8) swap_stage<32, 8>(a);
 #pragma unroll
   for (int k = 0; k < 16; ++k) v[k >> 3][k & 7] = a[k];
+}
+// (The usual 1024 without a test between the stages, each of which would copy
+// the 16 registers where its paths join.)
+__device__ __forceinline__ void fwht_block(float (&v)[2][8], int lhb) {
+  if (lhb == 10) fwht_stages(v, 10);
+  else fwht_stages(v, lhb);
 }
 // w[j]: the codes of piece j (dword h: register bit 2 set).
 __device__ __forceinline__ void fwht_order(uint2 (&w)[2], int lhb) {
@@ -282,7 +310,7 @@ struct RowCoder {
   // The codes of 8 values as two dwords. v r + 1.5 2^23 rounds v r to a whole
   // number, whose low byte is the sum's low byte. r is off by a rounding, so
   // that the product (at most 127) is off by at most 8e-6 from the quotient:
-  // only one nearer than 3e-5 to a half is decided by the quotient itself, in
+  // only one nearer than 1e-5 to a half is decided by the quotient itself, in
   // 64 bits (127 v is exact there, and a quotient of floats that is no tie is
   // further than 2^-33 from one).
   __device__ __forceinline__ uint2 codes(const float (&v)[8]) const {
@@ -295,7 +323,7 @@ struct RowCoder {
       u[i] = __float_as_uint(w);
       far = fmaxf(far, fabsf(fmaf(v[i], r, kWhole - w)));
     }
-    if (__builtin_amdgcn_ballot_w64(tiny || far > 0.49997f) != 0) {
+    if (__builtin_amdgcn_ballot_w64(tiny || far > 0.49999f) != 0) {
       asm volatile("");      // (a branch: computed anyway and selected, it took half of the kernel's time)
 #pragma unroll
       for (int i = 0; i < 8; ++i)

@@ -13,10 +13,12 @@
 namespace lq {
 namespace {
 
-// Wavefronts on a SIMD: two workgroups' registers have room (gated rows of
-// 28672), so that one loads while the other computes.
-template <int C, bool kXBF16, bool kGate>
-__global__ __launch_bounds__(1024, (C == 1 ? 8 : C == 2 ? 7 : 4)) void quant_rows_kernel(QuantRows p) {
+// Wavefronts on a SIMD: without T two workgroups' registers have room (gated
+// rows of 28672), so that one loads while the other computes. With T (kT) the
+// channel scales are loaded along with the row instead: few rows wait for
+// memory once, not twice.
+template <int C, bool kXBF16, bool kGate, bool kT>
+__global__ __launch_bounds__(1024, (C == 4 ? 4 : kT ? 5 : C == 2 ? 7 : 8)) void quant_rows_kernel(QuantRows p) {
   __shared__ float red[kRowMaxWaves];
   const int64_t b = blockIdx.x;
   const int K = (int)p.K;
@@ -30,6 +32,7 @@ __global__ __launch_bounds__(1024, (C == 1 ? 8 : C == 2 ? 7 : 4)) void quant_row
 #pragma unroll
   for (int i0 = 0; i0 < C; i0 += G) {
     RowPiece<kXBF16> x[G][2], g[G][2];
+    RowPiece<false> c[G][2];
     auto load = [&](auto wholec) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < G; ++i)
@@ -38,6 +41,12 @@ __global__ __launch_bounds__(1024, (C == 1 ? 8 : C == 2 ? 7 : 4)) void quant_row
           load_piece(x[i][j], xrow, row_col(i0 + i, j), K, decltype(wholec)::value);
           if constexpr (kGate) load_piece(g[i][j], grow, row_col(i0 + i, j), K, decltype(wholec)::value);
         }
+      if (kT && p.c != nullptr) {
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) load_piece(c[i][j], p.c, row_col(i0 + i, j), K, decltype(wholec)::value);
+      }
     };
     if (whole) load(std::true_type{});
     else load(std::false_type{});
@@ -45,34 +54,29 @@ __global__ __launch_bounds__(1024, (C == 1 ? 8 : C == 2 ? 7 : 4)) void quant_row
     for (int i = 0; i < G; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        float a[8];
         x[i][j].get(v[i0 + i][j]);
         if constexpr (kGate) {
-          float a[8];
           g[i][j].get(a);
           act_row8(p.act, a);
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[i0 + i][j][k] *= a[k];
         }
       }
+    if (kT && p.c != nullptr) {
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float a[8];
+          c[i][j].get(a);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i0 + i][j][k] *= a[k];
+        }
+    }
     if constexpr (C == 4) __builtin_amdgcn_sched_barrier(0);
   }
-  if (p.c != nullptr) {
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      RowPiece<false> c[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) load_piece(c[j], p.c, row_col(i, j), K, whole);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float a[8];
-        c[j].get(a);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][j][k] *= a[k];
-      }
-      if constexpr (C == 4) __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-  if (p.lhb > 0) {
+  if (kT && p.lhb > 0) {
 #pragma unroll
     for (int i = 0; i < C; ++i) fwht_block(v[i], p.lhb);
   }
@@ -89,22 +93,27 @@ __global__ __launch_bounds__(1024, (C == 1 ? 8 : C == 2 ? 7 : 4)) void quant_row
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     uint2 w[2] = {coder.codes(v[i][0]), coder.codes(v[i][1])};
-    if (p.lhb > 7) fwht_order(w, p.lhb);
+    if (kT && p.lhb > 7) fwht_order(w, p.lhb);
 #pragma unroll
     for (int j = 0; j < 2; ++j) store_codes(p.q + b * p.ldq, row_col(i, j), K, w[j]);
   }
   if (threadIdx.x == 0) p.scale[b] = coder.scale(p.norm);
 }
 
-template <int C>
+template <int C, bool kT>
 void enqueue(const QuantRows& p, dim3 grid, dim3 block, hipStream_t stream) {
   if (p.x_bf16) {
-    if (p.gate) hipLaunchKernelGGL((quant_rows_kernel<C, true, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((quant_rows_kernel<C, true, false>), grid, block, 0, stream, p);
+    if (p.gate) hipLaunchKernelGGL((quant_rows_kernel<C, true, true, kT>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((quant_rows_kernel<C, true, false, kT>), grid, block, 0, stream, p);
   } else {
-    if (p.gate) hipLaunchKernelGGL((quant_rows_kernel<C, false, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((quant_rows_kernel<C, false, false>), grid, block, 0, stream, p);
+    if (p.gate) hipLaunchKernelGGL((quant_rows_kernel<C, false, true, kT>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((quant_rows_kernel<C, false, false, kT>), grid, block, 0, stream, p);
   }
+}
+template <int C>
+void enqueue(const QuantRows& p, dim3 grid, dim3 block, hipStream_t stream) {
+  if (p.c != nullptr || p.lhb > 0) enqueue<C, true>(p, grid, block, stream);
+  else enqueue<C, false>(p, grid, block, stream);
 }
 
 }  // namespace
