@@ -56,10 +56,9 @@ __device__ __forceinline__ TilePlace tile_place(int t, int tiles_n, int tiles_b,
   return {grp * group_n + in % gn, in / gn};
 }
 
-// acc += a c with acc held in accumulation registers: left to itself the
-// compiler spreads 256 sums over both register files and spills. The
-// operands were waited for before the step's barrier; the readers of acc
-// wait for the last products (acc_ready).
+// acc += a c. The sums are pinned to accumulation registers where they begin
+// and where they are read (acc_take): left to itself the compiler spreads 256
+// of them over both register files and spills.
 __device__ __forceinline__ void mfma_acc(i32x4& acc, i32x4 a, i32x4 c) {
   acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, c, acc, 0, 0, 0);
 }
@@ -99,8 +98,8 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
   const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(place.n) * (32 * PN);
   const int64_t b0 = (int64_t)__builtin_amdgcn_readfirstlane(place.b) * (32 * PB);
 
-  const int K16 = ((int)p.K + 15) & ~15;
-  const int all = (K16 + KB - 1) / KB, full = K16 / KB;
+  const int K = (int)p.K, K16 = (K + 15) & ~15;
+  const int all = (K + KB - 1) / KB, full = K / KB;
   // This workgroup's steps: s0 .. steps - 1.
   const int s0 = (int)((int64_t)all * part_k / ksplit), steps = (int)((int64_t)all * (part_k + 1) / ksplit);
 
@@ -139,9 +138,17 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
   // The step that ends inside its KB bytes, if one of this workgroup's does.
   const int part = full < steps && full < all ? full : -1;
   auto zero_past = [&](uint4* st) __attribute__((always_inline)) {
-    if (KB * full + 16 * chunk < K16) return;
+    const int left = K - KB * full - 16 * chunk;       // of this lane's 16 codes, those that count
+    if (left >= 16) return;
+    uint32_t m[4];
 #pragma unroll
-    for (int k = kW; k < kCopies; ++k) st[(wave + 4 * k) * 64 + lane] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i)
+      m[i] = left >= 4 * i + 4 ? 0xFFFFFFFFu : left <= 4 * i ? 0u : (1u << (8 * (left - 4 * i))) - 1u;
+#pragma unroll
+    for (int k = kW; k < kCopies; ++k) {
+      uint4& c = st[(wave + 4 * k) * 64 + lane];
+      c = make_uint4(c.x & m[0], c.y & m[1], c.z & m[2], c.w & m[3]);
+    }
   };
   // Units of 16 bytes: row r's chunk 4 h + g (part h of the step, 64 bytes)
   // lies at kChunks r + ((4 h + g) ^ f(r)).
@@ -269,11 +276,11 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
       for (int j = 0; j < PB; ++j) o[(i * PB + j) * 64] = acc[i][j];
     return;
   }
-  // All scales are loaded before any output is
-  // stored. For bf16 two panels of rows are exchanged between lanes of the
-  // same token (the upper half of one with the lower half of the other, then
-  // odd rows of 16 lanes with even ones) so that lane g holds 8 consecutive
-  // outputs of the 32: a token's four lanes store 64 consecutive bytes.
+  // All scales are loaded before any output is stored. For bf16 two panels of
+  // rows are exchanged between lanes of the same token (the upper half of one
+  // with the lower half of the other, then odd rows of 16 lanes with even
+  // ones) so that lane g holds 8 consecutive outputs of the 32: a token's four
+  // lanes store 64 consecutive bytes.
   const int64_t nw = n0 + 16 * wn * PN, bw = b0 + 16 * wb * PB + r;
   float rs[PN][4], bias[PN][4], sb[PB];
 #pragma unroll

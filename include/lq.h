@@ -389,10 +389,10 @@ lq_status lq_linear_multi(const lq_layer* layers, int32_t n, const void* x, lq_d
  * Rows of these entry points may lie `ld` elements apart (ld >= K or N): a
  * slice of a wider product is taken as it is. Rows of x, gate, y and h need
  * only their element's alignment. 8-bit rows are padded to a multiple of 16
- * bytes: their ld is a multiple of 16, their first row is 16-byte aligned, every row
- * (the last too) owns its K rounded up to 16 bytes, and of q's rows the bytes
- * from K to there are zero (every entry point that writes q writes them so);
- * of w's rows those bytes may hold anything.
+ * bytes: their ld is a multiple of 16, their first row is 16-byte aligned and
+ * every row (the last too) owns its K rounded up to 16 bytes. What the bytes
+ * from K on hold does not matter to the product; lq_quant_rows and
+ * lq_norm_block write zeros there.
  */
 typedef enum lq_act {
   LQ_ACT_NONE = 0,

@@ -244,7 +244,8 @@ def make_layer(lq, rng, N, K, bias=False, ldw=None, extreme=False, **kw):
 
 
 def make_q(rng, B, K, ldq=None):
-    buf = torch.zeros(B, ldq or pad16(K), dtype=torch.int8, device=DEV)
+    """Random codes in rows whose pad bytes hold garbage."""
+    buf = torch.full((B, ldq or pad16(K)), 0x77, dtype=torch.int8, device=DEV)
     buf[:, :K] = torch.from_numpy(rng.integers(-128, 128, (B, K), dtype=np.int8)).to(DEV)
     return buf[:, :K]
 
