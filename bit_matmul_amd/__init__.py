@@ -370,6 +370,22 @@ def _vec(t, name: str, n: int):
     return ptr
 
 
+def _here(t, name: str):
+    """(address, bytes) of a workspace, or of none."""
+    if t is None:
+        return None, 0
+    ptr = _dev(t, name)
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return ptr, t.numel() * t.element_size()
+
+
+def _layer_here(layer: LQInt8Layer) -> None:
+    # (a struct filled by hand knows no device)
+    if getattr(layer, "device", None) not in (None, _current_device()):
+        raise ValueError(f"layer's tensors are on device {layer.device}, which is not the current one")
+
+
 def lq_quant_rows(x, B, K, q, scale, gate=None, act=LQ_ACT_NONE, hb=1, c=None, stream=None) -> None:
     """8-bit rows q (int8, rows padded to 16 bytes) and scale (float32) of
     T (act(gate) * x); x and gate: 2-D, of one dtype."""
@@ -390,8 +406,10 @@ def int8_layer_struct(N, K, w, row_scale, hb=1, c=None, bias=None) -> LQInt8Laye
     the tensors alive while the struct is used); w: int8, N rows of K, each
     padded to a multiple of 16 bytes."""
     wp, ldw = _rows8(w, "w", N, K)
-    return LQInt8Layer(N, K, ldw, hb, 0, wp, _vec(c, "c", K), _vec(row_scale, "row_scale", N),
-                       _vec(bias, "bias", N))
+    layer = LQInt8Layer(N, K, ldw, hb, 0, wp, _vec(c, "c", K), _vec(row_scale, "row_scale", N),
+                        _vec(bias, "bias", N))
+    layer.device = w.get_device()
+    return layer
 
 
 def lq_int8_gemm_workspace_size(layer: LQInt8Layer, B) -> int:
@@ -405,9 +423,10 @@ def lq_int8_gemm(layer: LQInt8Layer, q, scale, B, y, ws=None, stream=None) -> No
     """y = scale * row_scale * (q w^T) + bias for 8-bit rows q."""
     qp, ldq = _rows8(q, "q", B, layer.K)
     yp, ldy = _rows(y, "y", B, layer.N)
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    wsp, ws_bytes = _here(ws, "ws")
+    _layer_here(layer)
     _check(_lib.LIB.lq_int8_gemm(ctypes.byref(layer), qp, ldq, _vec(scale, "scale", B), B, yp,
-                                 _dtype(y, "y"), ldy, _opt(ws, "ws"), ws_bytes, _stream(stream)),
+                                 _dtype(y, "y"), ldy, wsp, ws_bytes, _stream(stream)),
            "lq_int8_gemm")
 
 
@@ -430,9 +449,10 @@ def lq_int8_linear(layer: LQInt8Layer, x, B, y, ws=None, stream=None) -> None:
     """The whole 8-bit layer: x to 8-bit rows, then the product."""
     xp, ldx = _rows(x, "x", B, layer.K)
     yp, ldy = _rows(y, "y", B, layer.N)
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    wsp, ws_bytes = _here(ws, "ws")
+    _layer_here(layer)
     _check(_lib.LIB.lq_int8_linear(ctypes.byref(layer), xp, _dtype(x, "x"), ldx, B, yp,
-                                   _dtype(y, "y"), ldy, _opt(ws, "ws"), ws_bytes, _stream(stream)),
+                                   _dtype(y, "y"), ldy, wsp, ws_bytes, _stream(stream)),
            "lq_int8_linear")
 
 

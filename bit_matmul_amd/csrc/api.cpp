@@ -99,6 +99,7 @@ static_assert(lq::kControlBytes == LQ_WS_CONTROL_BYTES, "control area size");
 static_assert(lq::kFusedErrorWord == LQ_WS_ERROR_WORD, "error word");
 static_assert(lq::kMultiMax == LQ_MULTI_MAX, "layers per grouped call");
 static_assert((size_t)LQ_INT8_MAX_K * 128 * 128 <= INT32_MAX, "a sum of byte products fits 32 bits");
+static_assert(lq::kRowMaxK == LQ_ROW_MAX_K, "longest row in registers");
 
 // Compute units of the current device (0 when there is none), cached.
 int device_cus() {
@@ -1165,7 +1166,7 @@ lq_status lq_norm_block(const lq_norm_block_args* a, void* stream) {
   if ((a->flags & ~kFlags) != 0 || !valid_act(a->act)) return LQ_ERR_INVALID_ARG;
   const bool post = a->flags & LQ_NORM_POST, pre = a->flags & LQ_NORM_PRE;
   const lq_dtype yt = (lq_dtype)a->ytype, ht = (lq_dtype)a->htype, at = (lq_dtype)a->atype;
-  if ((post || pre) && !(a->eps > 0.0f && std::isfinite(a->eps))) return LQ_ERR_INVALID_ARG;
+  if ((post || pre) && !(a->eps > 0.0f && std::isnormal(a->eps))) return LQ_ERR_INVALID_ARG;
   if (!std::isfinite(a->alpha)) return LQ_ERR_INVALID_ARG;
   if (a->y == nullptr && (a->gate != nullptr || post)) return LQ_ERR_INVALID_ARG;
   if ((a->q == nullptr) != (a->scale == nullptr)) return LQ_ERR_INVALID_ARG;

@@ -511,6 +511,10 @@ struct Int8Gemm {
   bool y_bf16;
 };
 // How a row kernel holds a row of K values: c blocks of 1024 in each wavefront.
+constexpr int kRowBlock = 1024;
+constexpr int kRowMaxWaves = 16;
+constexpr int kRowMaxC = 4;
+constexpr int64_t kRowMaxK = (int64_t)kRowBlock * kRowMaxWaves * kRowMaxC;
 struct RowShape {
   int c, waves;
 };

@@ -4,21 +4,16 @@
 // Layout: the row is cut into blocks of 1024 values; wavefront w of W takes
 // blocks w, w + W, ... (C of them). Of a block, lane l holds the values
 // 8 l .. 8 l + 7 and 512 + 8 l .. 512 + 8 l + 7: a wavefront's loads are
-// consecutive 16-byte pieces in the order of its lanes (pieces exchanged
-// within 64 bytes loaded a third slower), its 8-bit stores consecutive 8-byte
-// ones, and the index bits of a block are three register bits, six lane bits
-// and one register bit, so a Hadamard block of up to 1024 needs no LDS.
+// consecutive 16-byte pieces in the order of its lanes, its 8-bit stores
+// consecutive 8-byte ones, and the index bits of a block are three register
+// bits, six lane bits and one register bit, so a Hadamard block of up to 1024
+// needs no LDS.
 #pragma once
 
 #include "lq_internal.h"
 #include "lq_prep.h"
 
 namespace lq {
-
-constexpr int kRowBlock = 1024;
-constexpr int kRowMaxWaves = 16;
-constexpr int kRowMaxC = 4;
-constexpr int64_t kRowMaxK = (int64_t)kRowBlock * kRowMaxWaves * kRowMaxC;
 
 // Piece j (0, 1) of a thread's block i begins at column row_col(i, j), the
 // same for the wavefront, plus row_lane8(); row_whole: a wavefront's C blocks
@@ -145,22 +140,23 @@ __device__ __forceinline__ float row_reduce(float v, float* lds) {
 // The values of lq_act (include/lq.h).
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2, kActSigmoid = 3, kActTanh = 4;
 
-// 1 / (1 + exp(-x)) to a few units in the last place: exp as the hardware's
-// power of two of x log2(e), whose product is carried in two floats (one
-// float would lose |x| units), and one Newton step on the hardware's
-// reciprocal. Below -80 the value of -80 (2e-35) stands for what would
-// overflow the exponential.
+// 1 / (1 + exp(-x)) to a few units in the last place, from e = exp(-|x|),
+// which cannot overflow: 1 / (1 + e), and e times it where x is negative (so
+// that a large x times it vanishes as it should). exp is the hardware's power
+// of two of x log2(e), whose product is carried in two floats (one float
+// would lose |x| units); one Newton step on the hardware's reciprocal.
 __device__ __forceinline__ float sigmoid_f32(float x) {
   constexpr float kLog2e = 1.44269504088896340736f, kLog2eLo = 1.92596299112661746887e-8f;
-  const float m = x < -80.0f ? 80.0f : -x;
+  const float m = -fabsf(x);
   const float hi = m * kLog2e;
   const float lo = fmaf(m, kLog2e, -hi) + m * kLog2eLo;
-  // m of -inf (x = +inf): lo is NaN and exp2 of hi is zero
+  // (hi of an infinite x: lo is NaN, exp2 of hi is zero)
   float e = __builtin_amdgcn_exp2f(hi);
   e = hi > -126.0f ? fmaf(e, lo * 0.69314718055994530942f, e) : e;
   const float d = 1.0f + e;
-  const float r = __builtin_amdgcn_rcpf(d);
-  return fmaf(r, fmaf(-d, r, 1.0f), r);
+  float r = __builtin_amdgcn_rcpf(d);
+  r = fmaf(r, fmaf(-d, r, 1.0f), r);
+  return x < 0.0f ? e * r : r;
 }
 
 __device__ __forceinline__ float gelu_tanh_f32(float g) {

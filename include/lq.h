@@ -392,7 +392,8 @@ lq_status lq_linear_multi(const lq_layer* layers, int32_t n, const void* x, lq_d
  * bytes: their ld is a multiple of 16, their first row is 16-byte aligned and
  * every row (the last too) owns its K rounded up to 16 bytes. What the bytes
  * from K on hold does not matter to the product; lq_quant_rows and
- * lq_norm_block write zeros there.
+ * lq_norm_block write zeros there. Outputs overlap neither inputs nor each
+ * other, but where lq_norm_block says so.
  */
 typedef enum lq_act {
   LQ_ACT_NONE = 0,
@@ -424,8 +425,10 @@ typedef struct lq_int8_layer {
  * 8-bit rows q, scale of act(gate) .* x (formulas above). x: B rows of K in
  * xtype, ldx elements apart; gate: NULL, or rows of the same type ldg apart;
  * c: K channel scales or NULL, hb: as in lq_hadamard_scale; q: B rows, ldq
- * apart; scale: B floats. v is computed in fp32; the rounding to 8 bits is
- * that of the exact quotient. Errors: INVALID_ARG for a NULL or misaligned pointer, a
+ * apart; scale: B floats. v is computed in fp32,
+ * T's sums before their factor 1 / sqrt(hb) (a row where one of them passes
+ * the largest float counts as a row that holds an infinity); the rounding to
+ * 8 bits is that of the exact quotient. Errors: INVALID_ARG for a NULL or misaligned pointer, a
  * negative size, K < 1, ld below K, ldq not a multiple of 16, an unknown act
  * or dtype, hb not a power of two or not a divisor of K; UNSUPPORTED for
  * K > LQ_ROW_MAX_K, hb > LQ_MAX_HB or ldq > LQ_INT8_MAX_LD.
@@ -494,8 +497,8 @@ lq_status lq_int8_linear(const lq_int8_layer* layer, const void* x, lq_dtype xty
  * is needed); q and scale go together. ldg == 0: one gate for every row.
  * h_out may be h, and a may be y or h, with the same type and ld; nothing
  * else may overlap. Errors: INVALID_ARG as above, for both y and h NULL, a gate or
- * LQ_NORM_POST without y, h_out without htype, eps not positive and finite
- * with a norm, alpha not finite, unknown flags; UNSUPPORTED for K > LQ_ROW_MAX_K.
+ * LQ_NORM_POST without y, h_out without htype, eps not a positive normal
+ * float with a norm, alpha not finite, unknown flags; UNSUPPORTED for K > LQ_ROW_MAX_K.
  */
 #define LQ_NORM_POST 1u
 #define LQ_NORM_PRE 2u

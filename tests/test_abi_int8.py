@@ -156,7 +156,7 @@ NORM = dict(B=2, K=64, y=P, ldy=64, ytype=LQ_BF16, h=P, ldh=64, htype=LQ_BF16, h
     (dict(q=P, ldq=64), INV), (dict(scale=P), INV), (dict(q=P + 8, ldq=64, scale=P), INV),
     (dict(q=P, ldq=60, scale=P), INV), (dict(a=None, h_out=None), INV), (dict(w_pre=P + 2), INV),
     (dict(w_post=P + 1), INV), (dict(eps=0.0), INV), (dict(eps=float("nan")), INV),
-    (dict(eps=float("inf")), INV), (dict(eps=-1.0), INV), (dict(alpha=float("inf")), INV),
+    (dict(eps=float("inf")), INV), (dict(eps=1e-40), INV), (dict(eps=-1.0), INV), (dict(alpha=float("inf")), INV),
     (dict(alpha=float("nan")), INV), (dict(flags=16), INV), (dict(reserved=1), INV),
     (dict(B=0), LQ_OK),
 ])

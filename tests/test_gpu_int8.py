@@ -202,6 +202,28 @@ def test_gate_far_out(lq):
     near_codes(quant(lq, x, g, "gelu"), v, np.abs(v) * 20 * U32 + 1e-20)
 
 
+@pytest.mark.parametrize("act,size", [("silu", 1.0), ("silu", 3e36), ("gelu", 1.0), ("gelu", 3e36), ("sigmoid", 1e38)])
+def test_gate_far_below(lq, act, size):
+    """Gates that shut: act(g) x vanishes next to the row's largest value however large g or x are, and keeps
+    its relative accuracy while it is a normal float."""
+    g = torch.tensor([[-3e38, -1e38, -1e36, -1e30, -1e20, -1e9, -1e3, -150.0, -130.0, -20.0]], device=DEV)
+    x = torch.full_like(g, size)
+    x[0, 9] = 1.0
+    g64 = host64(g)
+    # (e^-130 times 1e38 or 130 3e36 is below 1e-17; the largest value is 2e-9 or more)
+    err = (gate_error(act, np.maximum(g64, -200.0)) + U32) * np.abs(ref.transform(host64(x), g64, act)) + 1e-17
+    if act == "gelu":
+        g[0, 9] = 1.0
+        g64 = host64(g)
+        err = np.full(g64.shape, 1e-6)
+    near_codes(quant(lq, x, g, act), ref.transform(host64(x), g64, act), err)
+    # a whole row of shut gates: e^-86 is a normal float
+    if act != "gelu":
+        g = torch.linspace(-80.0, -86.0, 40, device=DEV)[None]
+        v = ref.transform(np.ones((1, 40)), host64(g), act)
+        near_codes(quant(lq, torch.ones_like(g), g, act), v, np.abs(v) * (gate_error(act, host64(g)) + U32))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("hb", [1, 2, 4, 8, 16, 32, 64, 128, 256, 512, 1024])
 @pytest.mark.parametrize("B,blocks", [(2, 1), (1, 17)])
@@ -492,3 +514,88 @@ def test_int8_linear_is_the_transformed_layer(lq):
     # errors uniform within half a step: weights' steps are about 3.5 / 127 of a deviation, 0.8% of a weight;
     # a row's about 6 / 127 (the outlier spread over 512 adds 60 / sqrt(512) to a deviation of 1), under 1.4%
     assert np.linalg.norm(host64(y) - want) / np.linalg.norm(want) < 0.03
+
+
+# ------------------------------------------------------------------ far apart, and refused
+
+def far_rows(B, K, dtype, far):
+    """B rows of K, `far` elements apart (nothing between them is touched)."""
+    return torch.empty((B - 1) * far + pad16(K), dtype=dtype, device=DEV).as_strided((B, K), (far, 1))
+
+
+@pytest.mark.parametrize("B", [33, 530])
+def test_rows_behind_4_gb(lq, B):
+    """x, w, q and y whose last rows begin past 2^32 bytes: as the same rows lying together."""
+    rng = np.random.default_rng(B)
+    N, K = 540, 330
+    w, rs = torch.from_numpy(rng.integers(-127, 128, (N, K), dtype=np.int8)).to(DEV), randn(rng, N).abs()
+    x = randn(rng, B, K).to(BF)
+    q, s = rows8(B, K)[0], torch.empty(B, device=DEV)
+    wn = rows8(N, K)[0]
+    wn.copy_(w)
+    lq.lq_quant_rows(x, B, K, q, s)
+    want = torch.empty(B, N, device=DEV)
+    near = lq.int8_layer_struct(N, K, wn, rs)
+    n = lq.lq_int8_linear_workspace_size(near, B, BF)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    lq.lq_int8_linear(near, x, B, want, ws)
+    torch.cuda.synchronize()
+
+    wf = far_rows(N, K, torch.int8, 1 << 23)                      # 4.5 GB
+    wf.copy_(w)
+    layer = lq.int8_layer_struct(N, K, wf, rs)
+    far = (1 << 31) // (B - 1) // 16 * 16 + 1600                  # elements: 2^32 bytes of bf16
+    xf, yf = far_rows(B, K, BF, far), far_rows(B, N, F32, far)
+    xf.copy_(x)
+    note(f"lq_int8_linear far apart B={B} ld={far}")
+    lq.lq_int8_linear(layer, xf, B, yf, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(yf, want)
+    qf = far_rows(B, K, torch.int8, 1 << 23)                      # 4.4 GB where B is 530
+    sf = torch.empty_like(s)
+    note(f"lq_quant_rows far apart B={B}")
+    lq.lq_quant_rows(xf, B, K, qf, sf)
+    torch.cuda.synchronize()
+    assert torch.equal(qf, q) and torch.equal(sf, s)
+    yf.zero_()
+    note(f"lq_int8_gemm far apart B={B}")
+    lq.lq_int8_gemm(layer, qf, sf, B, yf, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(yf, want)
+
+
+def test_tensors_of_another_device_are_refused(lq):
+    rng = np.random.default_rng(31)
+    layer, keep = make_layer(lq, rng, 64, 96)
+    x, y = randn(rng, 2, 96), torch.zeros(2, 64, device=DEV)
+    ws = torch.empty(lq.lq_int8_linear_workspace_size(layer, 2, F32), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="ws must be a contiguous GPU tensor"):
+        lq.lq_int8_linear(layer, x, 2, y, ws)
+    with pytest.raises(ValueError, match="x must be a GPU tensor"):
+        lq.lq_int8_linear(layer, x.cpu(), 2, y, ws.to(DEV))
+    layer.device = 1
+    with pytest.raises(ValueError, match="not the current one"):
+        lq.lq_int8_linear(layer, x, 2, y, ws.to(DEV))
+    with pytest.raises(ValueError, match="not the current one"):
+        lq.lq_int8_gemm(layer, rows8(2, 96)[0], torch.ones(2, device=DEV), 2, y, ws.to(DEV))
+    assert torch.all(y == 0)
+
+
+def test_shared_rows_are_refused(lq):
+    """One row seen as many (a stride of zero) is no output, and no input of quant_rows."""
+    x = torch.ones(1, 64, device=DEV).expand(4, 64)
+    q, s = rows8(4, 64)[0], torch.empty(4, device=DEV)
+    with pytest.raises(RuntimeError):
+        lq.lq_quant_rows(x, 4, 64, q, s)
+    with pytest.raises(RuntimeError):
+        lq.lq_norm_block(4, 64, y=x.contiguous(), a=x)
+
+
+def test_transform_past_the_largest_float(lq):
+    """T's sums are taken before 1 / sqrt(hb): where one passes the largest float, the row is as one that
+    holds an infinity."""
+    x = torch.full((2, 1024), 1e36, device=DEV)
+    x[1] = 1e34
+    q, s = quant(lq, x, hb=1024)
+    assert np.isnan(s[0]) and np.all(q[0] == 0)
+    assert q[1, 0] == 127 and np.all(q[1, 1:] == 0) and abs(s[1] * 127 / 3.2e35 - 1) < 1e-6
