@@ -1100,7 +1100,7 @@ lq_status lq_int8_gemm_plan(const lq_int8_layer* layer, int64_t B, lq_int8_plan_
   if (s != LQ_OK) return s;
   if (B < 1 || layer->N < 1) return LQ_ERR_INVALID_ARG;
   const lq::Int8Plan p = int8_plan(layer, B);
-  *info = {32 * p.pn, 32 * p.pb, p.ksplit, p.tiles * p.ksplit};
+  *info = {p.rows, p.tokens, p.ksplit, p.tiles * p.ksplit};
   return LQ_OK;
 }
 

@@ -29,7 +29,8 @@
 // random codes, their 5 only on zeros.
 //
 // Few tiles: the reduction is split over ksplit workgroups, whose sums
-// int8_join_kernel adds (whole numbers: any order gives the same sum).
+// int8_join_kernel adds (whole numbers: any order gives the same sum). Up to
+// 16 tokens mostly take int8_few.hip's kernel instead.
 #include <type_traits>
 
 #include "lq_int8.h"
@@ -380,23 +381,27 @@ static void enqueue_tile(const Int8Gemm& p, const Int8Plan& plan, int* partial, 
                        stream, p, tn, tb, group_n, plan.ksplit, partial);
 }
 
-// The tiles (stages and bytes per step at the launches below), and what they
-// cost in us, fitted to 1100 measurements over 47 sizes (1 to 2048 tokens, 60
-// to 28672 outputs, 150 to 28672 inputs): a step takes `step` plus `share` for
-// every workgroup on the compute unit, a workgroup's begin and end take
-// `ends`. The choice it gives is on average 1.7% above the best of these
-// tiles and splits, 10% at most. Left out, with what their absence costs on
+// The tiles (stages and bytes per step at the launches below; with `few` those
+// of int8_few.hip, four steps at a time), and what they cost in us, fitted to
+// 2200 measurements over 157 sizes (1 to 2048 tokens, 60 to 60000 outputs, 150
+// to 28672 inputs): a step takes `step` plus `share` for every workgroup on
+// the compute unit, a workgroup's begin and end take `ends`. The choice it
+// gives is on average 1.7% above the best of these tiles and splits (0.7% up
+// to 16 tokens), 15% at most. Left out, with what their absence costs on
 // average: 32 x 64 tokens (0%), a 2-stage 32 x 32 (0.1%).
 struct TileCost {
-  int pn, pb, bytes, per_cu;
+  int rows, tokens, bytes, per_cu;
   float step, share, ends;
+  bool few;
 };
 static constexpr TileCost kTiles[] = {
-    {8, 8, 128, 1, 1.155f, 0.167f, 3.9f}, {7, 8, 128, 1, 0.932f, 0.262f, 3.1f},
-    {6, 8, 128, 1, 0.774f, 0.372f, 2.9f}, {4, 8, 128, 1, 0.925f, 0.033f, 2.8f},
-    {4, 4, 128, 1, 0.510f, 0.056f, 2.4f}, {4, 2, 256, 1, 0.803f, 0.016f, 1.6f},
-    {2, 4, 256, 1, 0.657f, 0.133f, 1.7f}, {2, 2, 256, 2, 0.532f, 0.202f, 1.4f},
-    {2, 1, 256, 3, 0.477f, 0.189f, 0.8f}, {1, 1, 256, 2, 0.180f, 0.168f, 1.1f},
+    {256, 256, 128, 1, 1.155f, 0.167f, 3.9f, false}, {224, 256, 128, 1, 0.932f, 0.262f, 3.1f, false},
+    {192, 256, 128, 1, 0.774f, 0.372f, 2.9f, false}, {128, 256, 128, 1, 0.925f, 0.033f, 2.8f, false},
+    {128, 128, 128, 1, 0.510f, 0.056f, 2.4f, false}, {128, 64, 256, 1, 0.803f, 0.016f, 1.6f, false},
+    {64, 128, 256, 1, 0.657f, 0.133f, 1.7f, false},  {64, 64, 256, 2, 0.532f, 0.202f, 1.4f, false},
+    {64, 32, 256, 3, 0.477f, 0.189f, 0.8f, false},   {32, 32, 256, 2, 0.180f, 0.168f, 1.1f, false},
+    {16, 4, 1024, 4, 0.102f, 0.386f, 1.3f, true},    {16, 8, 1024, 3, 0.088f, 0.372f, 1.3f, true},
+    {16, 16, 1024, 2, 0.096f, 0.581f, 1.2f, true},   {32, 16, 1024, 1, 0.007f, 1.146f, 1.6f, true},
 };
 constexpr float kJoinUs = 3.5f, kJoinBytesPerUs = 4.0e6f, kStreamBytesPerUs = 6.3e6f;
 constexpr int kMaxSplit = 16;
@@ -408,11 +413,12 @@ Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus) {
   Int8Plan best{};
   float best_us = 0.0f;
   for (const TileCost& c : kTiles) {
-    const int64_t tiles = ((N + 32 * c.pn - 1) / (32 * c.pn)) * ((B + 32 * c.pb - 1) / (32 * c.pb));
+    if (c.few && (B > c.tokens || (c.tokens > 4 && B <= c.tokens / 2))) continue;   // (no more codes than needed)
+    const int64_t tiles = ((N + c.rows - 1) / c.rows) * ((B + c.tokens - 1) / c.tokens);
     const int64_t slots = (int64_t)cus * c.per_cu, steps = (K + c.bytes - 1) / c.bytes;
     if (tiles > kMaxTiles && &c != kTiles) continue;
     for (int ks = 1; ks <= kMaxSplit && ks <= steps; ++ks) {
-      if (ks > 1 && tiles * ks > 4 * (int64_t)cus) break;
+      if (ks > 1 && (c.few || tiles * ks > 4 * (int64_t)cus)) break;
       const float len = (float)((steps + ks - 1) / ks);
       const int64_t units = tiles * ks, full = units / slots, rem = units % slots;
       float us = (float)full * (len * (c.step + c.share * c.per_cu) + c.ends);
@@ -421,10 +427,10 @@ Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus) {
         us += len * (c.step + c.share * load) + c.ends;
       }
       us = us > stream ? us + 0.3f * stream : stream + 0.3f * us;
-      const size_t partial = ks > 1 ? (size_t)units * c.pn * c.pb * 4096 : 0;
+      const size_t partial = ks > 1 ? (size_t)units * c.rows * c.tokens * 4 : 0;
       if (ks > 1) us += kJoinUs + 2.0f * (float)partial / kJoinBytesPerUs;
-      if (best.pn == 0 || us < best_us) {
-        best = {c.pn, c.pb, ks, (int)tiles, partial};
+      if (best.rows == 0 || us < best_us) {
+        best = {c.rows, c.tokens, ks, (int)tiles, c.few, partial};
         best_us = us;
       }
     }
@@ -434,7 +440,8 @@ Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus) {
 
 hipError_t launch_int8_gemm(const Int8Gemm& p, const Int8Plan& plan, int* partial, hipStream_t stream) {
   (void)hipGetLastError();   // clear a stale error of an earlier runtime call
-  switch (plan.pn * 16 + plan.pb) {
+  if (plan.few) return launch_int8_few(p, plan, stream);
+  switch (plan.rows / 32 * 16 + plan.tokens / 32) {
     case 0x88: enqueue_tile<8, 8, 2, 128>(p, plan, partial, stream); break;
     case 0x78: enqueue_tile<7, 8, 2, 128>(p, plan, partial, stream); break;
     case 0x68: enqueue_tile<6, 8, 2, 128>(p, plan, partial, stream); break;

@@ -521,15 +521,17 @@ struct RowShape {
 RowShape row_shape(int64_t K);
 hipError_t launch_quant_rows(const QuantRows& p, hipStream_t stream);
 hipError_t launch_norm_block(const NormBlock& p, hipStream_t stream);
-// How an 8-bit product runs: tiles of 32 pn weight rows x 32 pb tokens, the
-// reduction in ksplit parts.
+// How an 8-bit product runs: tiles of weight rows x tokens, the reduction in
+// ksplit parts (more than one: joined by a second launch).
 struct Int8Plan {
-  int pn, pb, ksplit, tiles;
+  int rows, tokens, ksplit, tiles;
+  bool few;               // int8_few.hip's kernel
   size_t partial_bytes;   // ksplit > 1: the parts' sums
 };
 Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus);
 // partial: Int8Plan::partial_bytes of workspace (unused when ksplit is 1).
 hipError_t launch_int8_gemm(const Int8Gemm& p, const Int8Plan& plan, int* partial, hipStream_t stream);
+hipError_t launch_int8_few(const Int8Gemm& p, const Int8Plan& plan, hipStream_t stream);
 // Rows and product of one token in one launch (t.q, t.scale and p.q, p.scale unused).
 bool int8_token_applies(const QuantRows& t, const Int8Plan& plan);
 hipError_t launch_int8_token(const QuantRows& t, const Int8Gemm& p, hipStream_t stream);

@@ -120,10 +120,10 @@ def test_int8_gemm_plan():
 def test_int8_gemm_workspace_is_checked():
     lay = layer(N=8192, K=28672, ldw=28672)
     n = ctypes.c_size_t()
-    assert LIB.lq_int8_gemm_workspace_size(lay, 16, ctypes.byref(n)) == LQ_OK and n.value > 0
+    assert LIB.lq_int8_gemm_workspace_size(lay, 64, ctypes.byref(n)) == LQ_OK and n.value > 0
 
     def f(ws, size):
-        return LIB.lq_int8_gemm(lay, P, 28672, P, 16, P, LQ_F32, 8192, ws, size, None)
+        return LIB.lq_int8_gemm(lay, P, 28672, P, 64, P, LQ_F32, 8192, ws, size, None)
     assert f(None, 0) == LQ_ERR_WORKSPACE
     assert f(P, n.value - 1) == LQ_ERR_WORKSPACE
     assert f(P + 8, n.value) == INV

@@ -342,8 +342,11 @@ def test_int8_gemm_largest_sum(lq, B):
 
 # (B, N, K, rows and tokens of the tile, whether the reduction is split)
 VARIANTS = [
-    (3, 16, 700, 32, 32, False), (1, 17, 6000, 32, 32, True), (1, 2000, 49, 64, 32, False),
-    (1, 6000, 12001, 64, 32, True), (129, 10001, 48, 64, 64, False), (33, 2000, 12001, 64, 64, True),
+    (20, 16, 700, 32, 32, False), (20, 17, 6000, 32, 32, True), (1, 2000, 49, 64, 32, False),
+    (20, 6000, 12001, 64, 32, True), (3, 16, 700, 16, 4, False), (4, 1001, 6001, 16, 4, False),
+    (2, 500, 300, 16, 4, False), (5, 3001, 5000, 16, 8, False), (8, 100, 1030, 16, 8, False),
+    (9, 2001, 3001, 16, 16, False), (16, 33, 2047, 16, 16, False), (16, 8185, 12001, 32, 16, False),
+    (13, 8001, 27000, 32, 16, False), (2, 256, 30001, 32, 32, True), (129, 10001, 48, 64, 64, False), (33, 2000, 12001, 64, 64, True),
     (100, 14000, 700, 64, 128, False), (1100, 100, 12001, 64, 128, True), (129, 10001, 300, 128, 64, False),
     (33, 3001, 12001, 128, 64, True), (129, 14000, 48, 128, 128, False), (65, 6000, 12001, 128, 128, True),
     (257, 14000, 48, 128, 256, False), (400, 5000, 12001, 128, 256, True), (513, 14000, 48, 192, 256, False),
