@@ -71,10 +71,10 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Gemm p) {
   static_assert((S - 1) * kCopies < 16, "the counter's low bits");
 
   i32x4 acc[kPanels] = {};
-  auto do_step = [&](int s, uint4* stage) __attribute__((always_inline)) {
+  // Of a step whose copies are in: its operands, then copies into its place,
+  // then its products. `last`: the step may end inside its 256 bytes.
+  auto do_step = [&](int s, uint4* stage, bool last) __attribute__((always_inline)) {
     i32x4 a[kPanels][4], c[4];
-    __builtin_amdgcn_s_waitcnt(kWaitVm);
-    __builtin_amdgcn_sched_barrier(0);
     const uint4* const in = stage + wave * kSize;
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Gemm p) {
       for (int i = 0; i < kPanels; ++i) a[i][h] = *reinterpret_cast<const i32x4*>(in + 16 * (16 * i + r) + at);
       c[h] = *reinterpret_cast<const i32x4*>(in + kW * 64 + 16 * (r % kTokens) + at);
     }
-    if (KB * (s + 1) > K) {
+    if (last && KB * (s + 1) > K) {
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const int left = K - KB * s - 16 * (4 * h + g);        // of these 16 codes, those that count
@@ -100,14 +100,21 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Gemm p) {
 #pragma unroll
       for (int i = 0; i < kPanels; ++i)
         acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i][h], c[h], acc[i], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(kWaitVm);          // the next step's copies are in
+    __builtin_amdgcn_sched_barrier(0);
   };
   copy_step(s0, stage0);
   copy_step(s0 + 1, stage1);
-  for (int s = s0; s < s1; ++s) {
-    do_step(s, stage0);
-    if (++s >= s1) break;
-    do_step(s, stage1);
+  __builtin_amdgcn_s_waitcnt(kWaitVm);
+  __builtin_amdgcn_sched_barrier(0);
+  int s = s0;
+  for (const int whole = min(s1, K / KB); s + S <= whole; s += S) {
+    do_step(s, stage0, false);
+    do_step(s + 1, stage1, false);
   }
+  if (s < s1) do_step(s, stage0, true);
+  if (s + 1 < s1) do_step(s + 1, stage1, true);
 
   // No copy may still be writing LDS when others write their sums there.
   __builtin_amdgcn_s_waitcnt(0);
