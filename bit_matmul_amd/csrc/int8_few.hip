@@ -9,15 +9,17 @@
 // their loads never stop together, and with 16 rows to a workgroup there are
 // enough of them that the reduction need not be split over a second launch.
 // Against tiles of 32 rows and 32 tokens with a barrier in each step and a
-// join (one token, product alone): 4096 x 14336 16.6 -> 13.5 us, 10240 x 8192
-// 22.7 -> 18.7, 8192 x 28672 49.0 -> 42.7 (5.5 TB/s), 1000 x 2050 5.8 -> 3.8.
+// join (one token, product alone): 4096 x 14336 16.6 -> 12.6 us, 10240 x 8192
+// 22.7 -> 18.9, 8192 x 28672 49.0 -> 43.5 (5.4 TB/s), 1000 x 2050 5.8 -> 3.8.
+// Three or four stages, fewer workgroups on a compute unit, gave nothing
+// (5125 x 4099 8.0 -> 8.3 and 8.6 us).
 //
 // Codes are copied for kTokens tokens only, 4, 8 or 16: columns of the
 // product that belong to none hold whatever was in LDS and are not stored.
 // Every 16 rows read the codes of their quarter again: at 16 tokens as many
-// bytes as weights, which is what two panels halve (8192 x 28672 48.8 -> 44.9
+// bytes as weights, which is what two panels halve (8192 x 28672 48.9 -> 45.0
 // us) where their workgroups, fewer and larger, still fill the device evenly
-// (10240 x 8192 22.2 -> 24.2).
+// (10240 x 8192 21.8 -> 24.2).
 //
 // Row r of a step keeps its 16-byte chunk c at 16 r + (c ^ (r & 15)), as in
 // int8_gemm.hip: no bank conflicts, whole lines copied.
@@ -70,11 +72,19 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Gemm p) {
   constexpr int kWaitLds0 = (3 << 14) | (7 << 4) | 15;
   static_assert((S - 1) * kCopies < 16, "the counter's low bits");
 
+  // Until the next step's copies at most are in flight. (The compiler waits
+  // for copies of its own accord before it reads where they went, and then
+  // for all of them. Only a wait that is followed by another instruction
+  // counts as one already done: hence the s_nop.)
+  auto wait_step = [&] __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(kWaitVm);
+    asm volatile("s_nop 0");
+    __builtin_amdgcn_sched_barrier(0);
+  };
   i32x4 acc[kPanels] = {};
-  // Of a step whose copies are in: its operands, then copies into its place,
-  // then its products. `last`: the step may end inside its 256 bytes.
   auto do_step = [&](int s, uint4* stage, bool last) __attribute__((always_inline)) {
     i32x4 a[kPanels][4], c[4];
+    wait_step();
     const uint4* const in = stage + wave * kSize;
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
@@ -100,14 +110,9 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Gemm p) {
 #pragma unroll
       for (int i = 0; i < kPanels; ++i)
         acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i][h], c[h], acc[i], 0, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(kWaitVm);          // the next step's copies are in
-    __builtin_amdgcn_sched_barrier(0);
   };
   copy_step(s0, stage0);
   copy_step(s0 + 1, stage1);
-  __builtin_amdgcn_s_waitcnt(kWaitVm);
-  __builtin_amdgcn_sched_barrier(0);
   int s = s0;
   for (const int whole = min(s1, K / KB); s + S <= whole; s += S) {
     do_step(s, stage0, false);

@@ -6,7 +6,7 @@
 // tokens. The reduction runs in steps of KB bytes, whole cache lines: 128 for
 // the large tiles, 256 for the small ones, whose time is that of the weights'
 // stream and grows shorter with the runs that a row is read in (27648 x 5120
-// at 64 tokens 39 -> 36 us; 64-byte steps took 51 us at 8192 x 28672, 16
+// at 64 tokens 39 -> 36 us, now 33; 64-byte steps took 51 us at 8192 x 28672, 16
 // tokens, where 128 and 256 take 47 and 46). A step's operands are blocks of
 // 1 KB, copied straight from memory to LDS (global_load_lds); S stages of LDS
 // hold the step in use and those being copied: as many as leave room for the
@@ -24,7 +24,7 @@
 // the copies of step s + S. Operands are read 64 bytes ahead, between the
 // products, and the copies are spread among the products: bunched up, they
 // filled the load unit's queue while the matrix cores waited (8192 x 28672 at
-// 2048 tokens 489 -> 404 us). There, 380 to 405 us (2.4 to 2.5 POP/s) of
+// 2048 tokens 489 -> 404 us). There, 370 to 385 us (2.5 to 2.6 POP/s) of
 // which the products alone take 305: the cores hold 3.4 to 3.6 POP/s on
 // random codes, their 5 only on zeros.
 //
@@ -248,10 +248,11 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
     __builtin_amdgcn_s_barrier();
     part_step(std::true_type{}, lane_at(s + S), cur, next, rd, a1, c1, a0, c0);
   };
-  // S steps at a time and one way out of the loop: with a test behind each
-  // step the compiler, which counts the copies in flight to wait for an
-  // array's before it is read, joined the ways out with the loop's next round
-  // and drained the copies in every round (512 tokens 8192 x 8192 50 -> 44 us).
+  // S steps at a time and one way out of the loop. (The compiler waits for
+  // copies of its own accord before it reads where they went, and then for all
+  // of them, unless the waits here have told it that they are in. With a test
+  // behind each step it lost count and drained them in every round: 512 tokens
+  // 8192 x 8192 50 us, not 44.)
   int s = s0;
   for (; s + S <= steps; s += S) {
     do_step(std::integral_constant<int, 0>{}, s);
@@ -391,10 +392,10 @@ static void enqueue_tile(const Int8Gemm& p, const Int8Plan& plan, int* partial, 
 // of int8_few.hip, four steps at a time), and what they cost in us, fitted to
 // 2200 measurements over 157 sizes (1 to 2048 tokens, 60 to 60000 outputs, 150
 // to 28672 inputs): a step takes `step` plus `share` for every workgroup on
-// the compute unit, a workgroup's begin and end take `ends`. The choice it
-// gives is on average 1.7% above the best of these tiles and splits (0.7% up
-// to 16 tokens), 15% at most. Left out, with what their absence costs on
-// average: 32 x 64 tokens (0%), a 2-stage 32 x 32 (0.1%).
+// the compute unit, a workgroup's begin and end take `ends`. Of 56 sizes the
+// choice it gives is on average 1.2% above the best of these tiles and splits,
+// 13% at most. Left out, with what their absence costs on average: 32 x 64
+// tokens (0%), a 2-stage 32 x 32 (0.1%).
 struct TileCost {
   int rows, tokens, bytes, per_cu;
   float step, share, ends;
