@@ -128,7 +128,11 @@ __device__ __forceinline__ float row_reduce(float v, float* lds) {
   if (waves == 1) return v;
   const int lane = threadIdx.x & 63;
   if (lane == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
+  // (A barrier for LDS alone: __syncthreads would wait for the loads in flight.)
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_s_waitcnt(3 << 14 | 7 << 4 | 15);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   v = (lane & 15) < waves ? lds[lane & 15] : Op::id();
   v = Op::of(v, lane_xor<1>(v));
   v = Op::of(v, lane_xor<2>(v));

@@ -462,7 +462,8 @@ def test_int8_linear_with_the_transform(lq, B):
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("N,K,hb", [(1, 1, 1), (33, 15, 1), (31, 257, 1), (500, 1000, 1), (32, 1024, 1024),
                                     (700, 4096, 128), (90, 4097, 1), (8200, 8192, 1024), (9001, 5121, 1),
-                                    (8225, 9216, 512), (8192, 16384, 1), (8193, 16385, 1), (10000, 16384, 64)])
+                                    (8225, 9216, 512), (8192, 16384, 1), (8193, 16385, 1), (10000, 16384, 64), (33001, 700, 1), (33000, 16, 1),
+                                    (8207, 1024, 1024), (9000, 256, 8), (1025, 2047, 1), (2049, 3000, 8)])
 def test_int8_linear_one_token(lq, N, K, hb, dtype):
     """One token: the bits of lq_quant_rows and lq_int8_gemm one after another, whichever path it takes."""
     rng = np.random.default_rng(N + K)
