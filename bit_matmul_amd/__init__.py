@@ -10,6 +10,7 @@ package fails.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -330,18 +331,20 @@ def lq_profile_events(starts, stops) -> None:
 def _rows(t, name: str, B: int, width: int):
     """(address, row stride in elements) of a 2-D GPU tensor whose rows are
     dense: a slice of a wider tensor is taken as it is."""
+    # (one test for a call that is right: a small call's time is the host's)
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.get_device() == _current_device():
+        rows, cols = t.shape
+        ld, step = t.stride()
+        if rows >= B and cols >= width and (step == 1 or width <= 1):
+            # (a single row's stride says nothing)
+            return t.data_ptr(), ld if rows > 1 or ld > width else width
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a GPU tensor of two dimensions")
-    rows, cols = t.shape
-    ld, step = t.stride()
-    if rows < B or cols < width:
+    if t.shape[0] < B or t.shape[1] < width:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {B} rows of {width} are needed")
     if t.get_device() != _current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    if step != 1 and width > 1:
-        raise ValueError(f"{name}'s rows must be dense")
-    # (a single row's stride says nothing)
-    return t.data_ptr(), ld if rows > 1 or ld > width else width
+    raise ValueError(f"{name}'s rows must be dense")
 
 
 def _rows8(t, name: str, B: int, K: int):
@@ -362,12 +365,13 @@ def _vec(t, name: str, n: int):
     """The address of n dense floats; None stays None."""
     if t is None:
         return None
+    if (t.dtype is torch.float32 and t.is_cuda and t.numel() >= n and t.is_contiguous() and
+            t.get_device() == _current_device()):
+        return t.data_ptr()
     if t.dtype != torch.float32 or t.numel() < n:
         raise ValueError(f"{name} must be {n} float32 values")
-    ptr = _dev(t, name)
-    if t.get_device() != _current_device():
-        raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return ptr
+    _dev(t, name)
+    raise ValueError(f"{name} is on {t.device}, which is not the current device")
 
 
 def _here(t, name: str):
@@ -456,6 +460,11 @@ def lq_int8_linear(layer: LQInt8Layer, x, B, y, ws=None, stream=None) -> None:
            "lq_int8_linear")
 
 
+_NORM_BLOCK_ARGS = struct.Struct("qq9Q6q4i2f2I")
+assert _NORM_BLOCK_ARGS.size == ctypes.sizeof(LQNormBlockArgs)
+_NORM_BLOCK = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, ctypes.c_void_p)(("lq_norm_block", _lib.LIB))
+
+
 def lq_norm_block(B, K, y=None, gate=None, act=LQ_ACT_NONE, gate_first=False, post=False,
                   w_post=None, h=None, alpha=1.0, h_out=None, pre=False, w_pre=None,
                   one_plus=False, eps=1e-5, a=None, q=None, scale=None, stream=None) -> None:
@@ -490,8 +499,8 @@ def lq_norm_block(B, K, y=None, gate=None, act=LQ_ACT_NONE, gate_first=False, po
         qp, ldq = _rows8(q, "q", B, K)
     flags = ((LQ_NORM_POST if post else 0) | (LQ_NORM_PRE if pre else 0) |
              (LQ_NORM_GATE_FIRST if gate_first else 0) | (LQ_NORM_ONE_PLUS if one_plus else 0))
-    # (in the order of the struct's fields)
-    p = LQNormBlockArgs(B, K, yp, gp, _vec(w_post, "w_post", K), hp, hop, _vec(w_pre, "w_pre", K), ap, qp,
-                        _vec(scale, "scale", B), ldy, ldg, ldh, ldho, lda, ldq, yt, ht, at, act, alpha, eps,
-                        flags, 0)
-    _check(_lib.LIB.lq_norm_block(ctypes.byref(p), _stream(stream)), "lq_norm_block")
+    # (packed in the order of the struct's fields: a third of the time that its constructor takes)
+    p = _NORM_BLOCK_ARGS.pack(B, K, yp or 0, gp or 0, _vec(w_post, "w_post", K) or 0, hp or 0, hop or 0,
+                              _vec(w_pre, "w_pre", K) or 0, ap or 0, qp or 0, _vec(scale, "scale", B) or 0,
+                              ldy, ldg, ldh, ldho, lda, ldq, yt, ht, at, act, alpha, eps, flags, 0)
+    _check(_NORM_BLOCK(p, _stream(stream)), "lq_norm_block")
