@@ -24,7 +24,7 @@
 // the copies of step s + S. Operands are read 64 bytes ahead, between the
 // products, and the copies are spread among the products: bunched up, they
 // filled the load unit's queue while the matrix cores waited (8192 x 28672 at
-// 2048 tokens 489 -> 404 us). There, 370 to 385 us (2.5 to 2.6 POP/s) of
+// 2048 tokens 489 -> 404 us). There, by now 340 to 370 us (2.6 to 2.8 POP/s), of
 // which the products alone take 305: the cores hold 3.4 to 3.6 POP/s on
 // random codes, their 5 only on zeros.
 //

@@ -1,4 +1,5 @@
-// Device helpers of the 8-bit product (int8_gemm.hip).
+// Device helpers of the 8-bit products (int8_gemm.hip, int8_few.hip,
+// int8_token.hip).
 #pragma once
 
 #include "lq_internal.h"

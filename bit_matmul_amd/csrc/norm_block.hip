@@ -12,6 +12,11 @@
 // the bytes. The second norm reads h' as it was summed in 32 bits, before it
 // is rounded to the residual stream's type. Squares are summed in 32 bits,
 // each thread its 16 C values, then a butterfly over lanes and wavefronts.
+//
+// Measured: 2048 rows of 8192 in bf16, both norms and 8-bit rows 27 us (4.4
+// TB/s), in fp32 without 8-bit rows 48 (5.6 TB/s); 777 rows of 4099 in fp32
+// with a gate 17 (3.7); one row 3.4 to 4.8 us (the launch, memory, two
+// reductions). Rows past 32768 (C = 4) spill: 256 of 40000 35 us, 2.3 TB/s.
 #include "lq_rows.h"
 
 namespace lq {
@@ -46,13 +51,12 @@ __device__ __forceinline__ float inv_rms(float (&v)[C][2][8], int K, float eps, 
   return 1.0f / sqrtf(s / (float)K);
 }
 
-// Rows of up to 16K (C = 1) load every tensor before the first reduction and
-// a norm's weights before its own: each reduction waits for the slowest
-// wavefront, and a load behind it would add the memory's latency once more.
-// All of it at the start cost more than it gave: with the registers of both
-// weights fewer workgroups fit (8192 channels, 2048 rows 31 -> 35 us).
-template <int C, bool kYBF16, bool kHBF16, bool kEarly>
-__global__ __launch_bounds__(1024, (C == 1 && !kEarly ? 8 : 4)) void norm_block_kernel(NormBlock p) {
+// Each tensor is loaded where it is first used. All loads before the first
+// reduction, which the registers of one block of 1024 have room for, gave
+// nothing for few rows (64 rows of 8192 with both norms 5.8 -> 6.0 us) and
+// cost many (2048 rows 26.9 -> 30.0 us: fewer workgroups fit).
+template <int C, bool kYBF16, bool kHBF16>
+__global__ __launch_bounds__(1024, (C == 1 ? 8 : 4)) void norm_block_kernel(NormBlock p) {
   __shared__ float red[5][kRowMaxWaves];
   const int64_t b = blockIdx.x;
   const int K = (int)p.K;
@@ -90,7 +94,7 @@ __global__ __launch_bounds__(1024, (C == 1 && !kEarly ? 8 : 4)) void norm_block_
   };
   auto gate = [&] __attribute__((always_inline)) {
     each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
-      if (!kEarly && j == 0) load(g, grow, i);
+      if (j == 0) load(g, grow, i);
       float a[8];
       g[j].get(a);
       act_row8(p.act, a);
@@ -100,25 +104,19 @@ __global__ __launch_bounds__(1024, (C == 1 && !kEarly ? 8 : 4)) void norm_block_
   };
   auto norm = [&](float* lds, const float* w) __attribute__((always_inline)) {
     RowPiece<false> wp[2];
-    if (kEarly) load_weights(wp, w, 0);
     const float r = inv_rms<C>(v, K, p.eps, lds);
     const float plus = p.one_plus ? 1.0f : 0.0f;
     each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
-      if (!kEarly && j == 0) load_weights(wp, w, i);
+      if (j == 0) load_weights(wp, w, i);
       float a[8];
       wp[j].get(a);
 #pragma unroll
       for (int k = 0; k < 8; ++k) u[k] = u[k] * r * (w != nullptr ? plus + a[k] : 1.0f);
     });
   };
-  if constexpr (kEarly) {
-    if (p.y != nullptr) load(y, yrow, 0);
-    if (p.gate != nullptr) load(g, grow, 0);
-    if (p.h != nullptr) load(h, hrow, 0);
-  }
   if (p.y != nullptr) {
     each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
-      if (!kEarly && j == 0) load(y, yrow, i);
+      if (j == 0) load(y, yrow, i);
       y[j].get(u);
     });
     if (p.gate != nullptr && p.gate_first) gate();
@@ -127,7 +125,7 @@ __global__ __launch_bounds__(1024, (C == 1 && !kEarly ? 8 : 4)) void norm_block_
   }
   if (p.h != nullptr) {
     each([&](float (&u)[8], int i, int j) __attribute__((always_inline)) {
-      if (!kEarly && j == 0) load(h, hrow, i);
+      if (j == 0) load(h, hrow, i);
       float a[8];
       h[j].get(a);
 #pragma unroll
@@ -163,16 +161,14 @@ __global__ __launch_bounds__(1024, (C == 1 && !kEarly ? 8 : 4)) void norm_block_
   }
 }
 
-constexpr int64_t kEarlyRows = 256;
-
-template <int C, bool kEarly>
+template <int C>
 void enqueue(const NormBlock& p, dim3 grid, dim3 block, hipStream_t stream) {
   if (p.y_bf16) {
-    if (p.h_bf16) hipLaunchKernelGGL((norm_block_kernel<C, true, true, kEarly>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((norm_block_kernel<C, true, false, kEarly>), grid, block, 0, stream, p);
+    if (p.h_bf16) hipLaunchKernelGGL((norm_block_kernel<C, true, true>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((norm_block_kernel<C, true, false>), grid, block, 0, stream, p);
   } else {
-    if (p.h_bf16) hipLaunchKernelGGL((norm_block_kernel<C, false, true, kEarly>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((norm_block_kernel<C, false, false, kEarly>), grid, block, 0, stream, p);
+    if (p.h_bf16) hipLaunchKernelGGL((norm_block_kernel<C, false, true>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((norm_block_kernel<C, false, false>), grid, block, 0, stream, p);
   }
 }
 
@@ -182,10 +178,9 @@ hipError_t launch_norm_block(const NormBlock& p, hipStream_t stream) {
   (void)hipGetLastError();   // clear a stale error of an earlier runtime call
   const RowShape s = row_shape(p.K);
   const dim3 grid((unsigned)p.B), block(64u * (unsigned)s.waves);
-  if (s.c == 1 && p.B <= kEarlyRows) enqueue<1, true>(p, grid, block, stream);
-  else if (s.c == 1) enqueue<1, false>(p, grid, block, stream);
-  else if (s.c == 2) enqueue<2, false>(p, grid, block, stream);
-  else enqueue<4, false>(p, grid, block, stream);
+  if (s.c == 1) enqueue<1>(p, grid, block, stream);
+  else if (s.c == 2) enqueue<2>(p, grid, block, stream);
+  else enqueue<4>(p, grid, block, stream);
   return hipGetLastError();
 }
 

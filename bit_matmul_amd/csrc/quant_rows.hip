@@ -5,7 +5,9 @@
 //
 // One workgroup per row, the row in registers (lq_rows.h): it is read once,
 // its maximum is one reduction over the workgroup, and the codes are written
-// from the same registers. The time is that of the bytes.
+// from the same registers. The time is that of the bytes: 2048 rows of 8192 in
+// bf16 16 us (3.1 TB/s), of 28672 44 (4.0 TB/s), gated 68 (4.3 TB/s); with T
+// 18 and 66. One row of 8192 3.9 us.
 #include <type_traits>
 
 #include "lq_rows.h"
