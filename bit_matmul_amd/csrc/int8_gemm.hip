@@ -13,8 +13,10 @@
 // workgroups that share a compute unit.
 //
 // Row r of a panel keeps its 16-byte chunk c at KB r + 16 (c ^ f(r)), f(r) =
-// (r & 7) ^ (r >> 3) for 8 chunks, r for 16: any 8 lanes of consecutive rows
-// that read the same chunk then touch 32 different banks, any 16 touch 64.
+// (r & 7) ^ (r >> 3) for 8 chunks, r for 16: any 16 lanes that read the same
+// chunk then touch 64 different banks. (The counters show no conflicts for 16
+// chunks, and for 8 some, in 18% of the cycles: lanes of two chunks are read
+// together. A form of f without any took the same time.)
 // The copy of a block puts lane l's 16 bytes at 16 l, so lanes in turn read
 // the chunks of one row in the order that f gives: whole lines.
 //
@@ -25,8 +27,9 @@
 // products, and the copies are spread among the products: bunched up, they
 // filled the load unit's queue while the matrix cores waited (8192 x 28672 at
 // 2048 tokens 489 -> 404 us). There, by now 340 to 370 us (2.6 to 2.8 POP/s), of
-// which the products alone take 305: the cores hold 3.4 to 3.6 POP/s on
-// random codes, their 5 only on zeros.
+// which the products alone take 280 to 305 and the copies alone 297: the cores
+// are busy for 72% of the cycles, at the 1.9 GHz that the card's power leaves
+// (alone they hold 3.4 to 3.6 POP/s on random codes, 5 only on zeros).
 //
 // Few tiles: the reduction is split over ksplit workgroups, whose sums
 // int8_join_kernel adds (whole numbers: any order gives the same sum). Up to
