@@ -1035,7 +1035,8 @@ struct Int8Ws {
 Int8Ws int8_ws(const lq_int8_layer* l, int64_t B) {
   Int8Ws w;
   w.plan = int8_plan(l, B);
-  w.ldq = round16(l->K);
+  // whole cache lines: rows at other places are read in one line more each time
+  w.ldq = (l->K + 127) & ~int64_t(127);
   w.off_q = align_up(lq::kControlBytes);
   w.off_scale = w.off_q + align_up((size_t)B * w.ldq);
   w.off_partial = w.off_scale + align_up((size_t)B * sizeof(float));

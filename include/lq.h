@@ -392,8 +392,9 @@ lq_status lq_linear_multi(const lq_layer* layers, int32_t n, const void* x, lq_d
  * bytes: their ld is a multiple of 16, their first row is 16-byte aligned and
  * every row (the last too) owns its K rounded up to 16 bytes. What the bytes
  * from K on hold does not matter to the product; lq_quant_rows and
- * lq_norm_block write zeros there. Outputs overlap neither inputs nor each
- * other, but where lq_norm_block says so.
+ * lq_norm_block write zeros there. Rows at multiples of 128 bytes are read
+ * fastest (up to a tenth of a product's time). Outputs overlap neither inputs
+ * nor each other, but where lq_norm_block says so.
  */
 typedef enum lq_act {
   LQ_ACT_NONE = 0,
