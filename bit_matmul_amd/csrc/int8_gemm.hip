@@ -393,12 +393,13 @@ static void enqueue_tile(const Int8Gemm& p, const Int8Plan& plan, int* partial, 
 
 // The tiles (stages and bytes per step at the launches below; with `few` those
 // of int8_few.hip, four steps at a time), and what they cost in us, fitted to
-// 2200 measurements over 157 sizes (1 to 2048 tokens, 60 to 60000 outputs, 150
+// 2400 measurements over 180 sizes (1 to 2048 tokens, 60 to 200000 outputs, 150
 // to 28672 inputs): a step takes `step` plus `share` for every workgroup on
-// the compute unit, a workgroup's begin and end take `ends`. Of 56 sizes the
-// choice it gives is on average 1.2% above the best of these tiles and splits,
-// 13% at most. Left out, with what their absence costs on average: 32 x 64
-// tokens (0%), a 2-stage 32 x 32 (0.1%).
+// the compute unit, a workgroup's begin and end take `ends`, and the weights'
+// stream, at the rate that its kernel reaches, hides all but kHidden of that
+// (or is hidden by it). Of these sizes the choice it gives is on average 0.8%
+// above the best of these tiles and splits, 12% at most. Left out, with what
+// their absence costs on average: 32 x 64 tokens (0%), a 2-stage 32 x 32 (0.1%).
 struct TileCost {
   int rows, tokens, bytes, per_cu;
   float step, share, ends;
@@ -407,24 +408,25 @@ struct TileCost {
 static constexpr TileCost kTiles[] = {
     {256, 256, 128, 1, 1.155f, 0.167f, 3.9f, false}, {224, 256, 128, 1, 0.932f, 0.262f, 3.1f, false},
     {192, 256, 128, 1, 0.774f, 0.372f, 2.9f, false}, {128, 256, 128, 1, 0.925f, 0.033f, 2.8f, false},
-    {128, 128, 128, 1, 0.510f, 0.056f, 2.4f, false}, {128, 64, 256, 1, 0.803f, 0.016f, 1.6f, false},
-    {64, 128, 256, 1, 0.657f, 0.133f, 1.7f, false},  {64, 64, 256, 2, 0.532f, 0.202f, 1.4f, false},
-    {64, 32, 256, 3, 0.477f, 0.189f, 0.8f, false},   {32, 32, 256, 2, 0.180f, 0.168f, 1.1f, false},
-    {16, 4, 1024, 4, 0.102f, 0.386f, 1.3f, true},    {16, 8, 1024, 3, 0.088f, 0.372f, 1.3f, true},
-    {16, 16, 1024, 2, 0.096f, 0.581f, 1.2f, true},   {32, 16, 1024, 1, 0.007f, 1.146f, 1.6f, true},
+    {128, 128, 128, 1, 0.469f, 0.058f, 2.6f, false}, {128, 64, 256, 1, 0.829f, 0.013f, 2.2f, false},
+    {64, 128, 256, 1, 0.530f, 0.323f, 2.1f, false},  {64, 64, 256, 2, 0.728f, 0.225f, 1.5f, false},
+    {64, 32, 256, 3, 0.424f, 0.190f, 1.74f, false},  {32, 32, 256, 2, 0.140f, 0.202f, 1.36f, false},
+    {16, 4, 1024, 4, 0.369f, 0.511f, 0.72f, true},   {16, 8, 1024, 3, 0.072f, 0.672f, 0.81f, true},
+    {16, 16, 1024, 2, 0.112f, 0.593f, 1.12f, true},  {32, 16, 1024, 1, 0.007f, 1.171f, 1.45f, true},
 };
-constexpr float kJoinUs = 3.5f, kJoinBytesPerUs = 4.0e6f, kStreamBytesPerUs = 6.3e6f;
+constexpr float kJoinUs = 5.0f, kJoinBytesPerUs = 7.0e6f;
+constexpr float kStreamBytesPerUs[2] = {4.72e6f, 6.3e6f}, kHidden[2] = {0.216f, 0.298f};     // tiles, few
 constexpr int kMaxSplit = 16;
 constexpr int64_t kMaxTiles = 1 << 22;    // (a launch has fewer than 2^32 threads)
 
 Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus) {
   if (cus <= 0) cus = 256;
-  const float stream = (float)N * (float)K / kStreamBytesPerUs;      // the weights' stream
   Int8Plan best{};
   float best_us = 0.0f;
   for (const TileCost& c : kTiles) {
     if (c.few && (B > c.tokens || (c.tokens > 4 && B <= c.tokens / 2))) continue;   // (no more codes than needed)
     const int64_t tiles = ((N + c.rows - 1) / c.rows) * ((B + c.tokens - 1) / c.tokens);
+    const float stream = (float)N * (float)K / kStreamBytesPerUs[c.few];      // the weights'
     const int64_t slots = (int64_t)cus * c.per_cu, steps = (K + c.bytes - 1) / c.bytes;
     if (tiles > kMaxTiles && &c != kTiles) continue;
     for (int ks = 1; ks <= kMaxSplit && ks <= steps; ++ks) {
@@ -436,7 +438,7 @@ Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus) {
         const float load = 0.5f * ((float)rem / cus + (float)((rem + cus - 1) / cus));
         us += len * (c.step + c.share * load) + c.ends;
       }
-      us = us > stream ? us + 0.3f * stream : stream + 0.3f * us;
+      us = us > stream ? us + kHidden[c.few] * stream : stream + kHidden[c.few] * us;
       const size_t partial = ks > 1 ? (size_t)units * c.rows * c.tokens * 4 : 0;
       if (ks > 1) us += kJoinUs + 2.0f * (float)partial / kJoinBytesPerUs;
       if (best.rows == 0 || us < best_us) {

@@ -340,17 +340,36 @@ def test_int8_gemm_largest_sum(lq, B):
     assert torch.all(y > 0)
 
 
+@pytest.mark.parametrize("B", [1, 7, 16])
+def test_int8_gemm_largest_sum_of_few_tokens(lq, B):
+    """The same with enough rows that the reduction is not split: four wavefronts' parts of it meet."""
+    N, K = 8192, lq.LQ_INT8_MAX_K
+    w = torch.full((N, pad16(K)), -128, dtype=torch.int8, device=DEV)
+    w[N - 1] = 127
+    q = torch.full((B, pad16(K)), -128, dtype=torch.int8, device=DEV)
+    one = torch.ones(N, device=DEV)
+    layer = lq.int8_layer_struct(N, K, w[:, :K], one)
+    assert lq.lq_int8_gemm_plan(layer, B)["tokens"] <= 16
+    y = torch.zeros(B, N, device=DEV)
+    note(f"lq_int8_gemm largest sum B={B} N={N}")
+    lq.lq_int8_gemm(layer, q[:, :K], one[:B], B, y, garbage(lq.lq_int8_gemm_workspace_size(layer, B)))
+    torch.cuda.synchronize()
+    assert torch.all(y[:, :N - 1] == float(np.float32(K * 128 * 128)))
+    assert torch.all(y[:, N - 1] == float(np.float32(-K * 128 * 127)))
+
+
 # (B, N, K, rows and tokens of the tile, whether the reduction is split)
 VARIANTS = [
-    (20, 16, 700, 32, 32, False), (20, 17, 6000, 32, 32, True), (1, 2000, 49, 64, 32, False),
-    (20, 6000, 12001, 64, 32, True), (3, 16, 700, 16, 4, False), (4, 1001, 6001, 16, 4, False),
+    (20, 16, 700, 32, 32, False), (20, 17, 6000, 32, 32, True), (17, 20001, 48, 64, 32, False),
+    (33, 1001, 20001, 64, 32, True), (3, 16, 700, 16, 4, False), (4, 1001, 6001, 16, 4, False),
     (2, 500, 300, 16, 4, False), (5, 3001, 5000, 16, 8, False), (8, 100, 1030, 16, 8, False),
     (9, 2001, 3001, 16, 16, False), (16, 33, 2047, 16, 16, False), (16, 8185, 12001, 32, 16, False),
-    (13, 8001, 27000, 32, 16, False), (2, 256, 30001, 32, 32, True), (129, 10001, 48, 64, 64, False), (33, 2000, 12001, 64, 64, True),
-    (100, 14000, 700, 64, 128, False), (1100, 100, 12001, 64, 128, True), (129, 10001, 300, 128, 64, False),
+    (13, 8001, 27000, 32, 16, False), (2, 256, 30001, 32, 32, True), (129, 10001, 48, 64, 64, False),
+    (33, 2000, 12001, 128, 64, True),
+    (100, 14000, 700, 64, 128, False), (1100, 100, 12001, 64, 128, True), (129, 10001, 700, 128, 64, False),
     (33, 3001, 12001, 128, 64, True), (129, 14000, 48, 128, 128, False), (65, 6000, 12001, 128, 128, True),
-    (257, 14000, 48, 128, 256, False), (400, 5000, 12001, 128, 256, True), (513, 14000, 48, 192, 256, False),
-    (400, 10001, 12001, 192, 256, True), (1100, 10001, 48, 224, 256, False), (257, 14000, 12001, 224, 256, True),
+    (257, 14000, 48, 128, 256, False), (400, 3001, 12001, 128, 256, True), (513, 14000, 48, 192, 256, False),
+    (513, 4001, 12001, 192, 256, True), (1100, 10001, 48, 224, 256, False), (257, 14000, 12001, 224, 256, True),
     (1500, 10001, 48, 256, 256, False), (1100, 4000, 14336, 256, 256, True),
 ]
 
