@@ -74,10 +74,19 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return _DTYPES[t.dtype]
 
 
+def _public_device() -> int:
+    return torch.cuda.current_device()
+
+
+def _public_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 # The current device, and the handle of its current stream without a stream
-# object around it (that object costs 3 us of a call's 10).
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# object around it (that object costs 3 us of a call's 10). The short way is
+# private to torch: one that lacks it is asked through its public functions.
+_current_device = getattr(torch._C, "_cuda_getDevice", _public_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
 
 
 def _stream(stream) -> int:
