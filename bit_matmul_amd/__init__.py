@@ -39,7 +39,8 @@ __all__ = [
     "lq_linear_plan", "lq_sign_gemm_plan", "lq_workspace_status", "lq_debug_fused_timeout",
     "LQ_ERR_DEVICE", "LQ_MAX_L", "LQPlanInfo",
     "lq_quant_rows", "int8_layer_struct", "lq_int8_gemm_workspace_size", "lq_int8_gemm",
-    "lq_int8_linear_workspace_size", "lq_int8_linear", "lq_int8_gemm_plan", "lq_norm_block",
+    "lq_int8_linear_workspace_size", "lq_int8_linear", "lq_int8_gemm_plan", "lq_int8_linear_plan",
+    "lq_norm_block",
     "LQInt8Layer", "LQInt8PlanInfo",
     "LQNormBlockArgs", "LQ_ACT_NONE", "LQ_ACT_SILU", "LQ_ACT_GELU", "LQ_ACT_SIGMOID",
     "LQ_ACT_TANH", "LQ_NORM_POST", "LQ_NORM_PRE", "LQ_NORM_GATE_FIRST", "LQ_NORM_ONE_PLUS",
@@ -443,11 +444,20 @@ def lq_int8_gemm(layer: LQInt8Layer, q, scale, B, y, ws=None, stream=None) -> No
            "lq_int8_gemm")
 
 
+def _int8_plan(name: str, layer: LQInt8Layer, B) -> dict:
+    info = LQInt8PlanInfo()
+    _check(getattr(_lib.LIB, name)(ctypes.byref(layer), B, ctypes.byref(info)), name)
+    return {f: getattr(info, f) for f, _ in LQInt8PlanInfo._fields_}
+
+
 def lq_int8_gemm_plan(layer: LQInt8Layer, B) -> dict:
     """Tile and split of the reduction that lq_int8_gemm would use."""
-    info = LQInt8PlanInfo()
-    _check(_lib.LIB.lq_int8_gemm_plan(ctypes.byref(layer), B, ctypes.byref(info)), "lq_int8_gemm_plan")
-    return {f: getattr(info, f) for f, _ in LQInt8PlanInfo._fields_}
+    return _int8_plan("lq_int8_gemm_plan", layer, B)
+
+
+def lq_int8_linear_plan(layer: LQInt8Layer, B) -> dict:
+    """The same of lq_int8_linear; tokens is 1 where one token takes one launch."""
+    return _int8_plan("lq_int8_linear_plan", layer, B)
 
 
 def lq_int8_linear_workspace_size(layer: LQInt8Layer, B, xtype) -> int:

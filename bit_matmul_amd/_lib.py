@@ -40,7 +40,7 @@ EXPORTS = [
     "lq_workspace_status", "lq_debug_fused_timeout", "lq_encode_pinv_workspace_size",
     "lq_encode_pinv", "lq_quant_rows", "lq_int8_gemm_workspace_size", "lq_int8_gemm",
     "lq_int8_linear_workspace_size", "lq_int8_linear", "lq_norm_block",
-    "lq_int8_gemm_plan",
+    "lq_int8_gemm_plan", "lq_int8_linear_plan",
 ]
 
 
@@ -146,6 +146,7 @@ def _load():
         "lq_int8_linear": (c_int, [POINTER(LQInt8Layer), vp, c_int, i64, i64, vp, c_int, i64, vp,
                                    sz, vp]),
         "lq_int8_gemm_plan": (c_int, [POINTER(LQInt8Layer), i64, POINTER(LQInt8PlanInfo)]),
+        "lq_int8_linear_plan": (c_int, [POINTER(LQInt8Layer), i64, POINTER(LQInt8PlanInfo)]),
         "lq_norm_block": (c_int, [POINTER(LQNormBlockArgs), vp]),
     }
     for name, (res, args) in protos.items():

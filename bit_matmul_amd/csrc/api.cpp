@@ -1131,6 +1131,23 @@ lq_status lq_int8_linear_workspace_size(const lq_int8_layer* layer, int64_t B, l
   return LQ_OK;
 }
 
+lq_status lq_int8_linear_plan(const lq_int8_layer* layer, int64_t B, lq_int8_plan_info* info) {
+  if (info == nullptr) return LQ_ERR_INVALID_ARG;
+  lq_status s = check_int8_layer(layer, B, LQ_ROW_MAX_K);
+  if (s != LQ_OK) return s;
+  if (B < 1 || layer->N < 1) return LQ_ERR_INVALID_ARG;
+  const lq::Int8Plan plan = int8_plan(layer, B);
+  lq::QuantRows p{};
+  p.B = B;
+  p.K = layer->K;
+  fill_hb(&p, layer->hb);
+  if (const int rows = lq::int8_token_rows(p, layer->N, plan); rows > 0)
+    *info = {rows, 1, 1, (int32_t)((layer->N + rows - 1) / rows)};
+  else
+    *info = {plan.rows, plan.tokens, plan.ksplit, plan.tiles * plan.ksplit};
+  return LQ_OK;
+}
+
 lq_status lq_int8_linear(const lq_int8_layer* layer, const void* x, lq_dtype xtype, int64_t ldx,
                          int64_t B, void* y, lq_dtype ytype, int64_t ldy, void* ws,
                          size_t ws_bytes, void* stream) {
@@ -1152,8 +1169,8 @@ lq_status lq_int8_linear(const lq_int8_layer* layer, const void* x, lq_dtype xty
                   xtype == LQ_BF16};
   fill_hb(&p, layer->hb);
   const lq::Int8Gemm gemm = gemm_args(layer, q, w.ldq, scale, B, y, ytype, ldy);
-  if (lq::int8_token_applies(p, w.plan))
-    return hip_status(lq::launch_int8_token(p, gemm, (hipStream_t)stream));
+  if (const int rows = lq::int8_token_rows(p, layer->N, w.plan); rows > 0)
+    return hip_status(lq::launch_int8_token(p, gemm, rows, (hipStream_t)stream));
   s = hip_status(lq::launch_quant_rows(p, (hipStream_t)stream));
   if (s != LQ_OK) return s;
   return hip_status(lq::launch_int8_gemm(gemm, w.plan,

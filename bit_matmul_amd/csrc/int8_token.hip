@@ -171,10 +171,15 @@ __global__ __launch_bounds__(256) void int8_token_kernel(QuantRows t, Int8Gemm p
 
 }  // namespace
 
-// One token, no gate, a short row, and a product that need not split its
-// reduction to fill the device (that is a launch more, as this is one less).
-bool int8_token_applies(const QuantRows& t, const Int8Plan& plan) {
-  return t.B == 1 && t.gate == nullptr && t.K <= 4 * kRowBlock && plan.ksplit == 1;
+// One token, no gate, a short row, a product that need not split its
+// reduction to fill the device (that is a launch more, as this is one less),
+// and rows for fewer than 2^24 workgroups of 256 (a launch has fewer than 2^32
+// threads; the tiles of more rows take more of them).
+int int8_token_rows(const QuantRows& t, int64_t N, const Int8Plan& plan) {
+  if (t.B != 1 || t.gate != nullptr || t.K > 4 * kRowBlock || plan.ksplit != 1) return 0;
+  const int64_t many = t.lhb > 0 ? 8192 : 32768;      // rows from which on two panels pay (see the top)
+  const int rows = t.K <= kRowBlock && N > many ? 32 : 16;
+  return (N + rows - 1) / rows < (1 << 24) ? rows : 0;
 }
 
 template <int S, int kPanels>
@@ -184,10 +189,9 @@ static void enqueue_token(const QuantRows& t, const Int8Gemm& p, hipStream_t str
   else hipLaunchKernelGGL((int8_token_kernel<false, S, kPanels>), grid, dim3(256), 0, stream, t, p);
 }
 
-hipError_t launch_int8_token(const QuantRows& t, const Int8Gemm& p, hipStream_t stream) {
+hipError_t launch_int8_token(const QuantRows& t, const Int8Gemm& p, int rows, hipStream_t stream) {
   (void)hipGetLastError();   // clear a stale error of an earlier runtime call
-  const int64_t many = t.lhb > 0 ? 8192 : 32768;      // rows from which on two panels pay (see the top)
-  if (t.K <= kRowBlock && p.N > many) enqueue_token<1, 2>(t, p, stream);
+  if (rows == 32) enqueue_token<1, 2>(t, p, stream);
   else if (t.K <= kRowBlock) enqueue_token<1, 1>(t, p, stream);
   else if (t.K <= 2 * kRowBlock) enqueue_token<2, 1>(t, p, stream);
   else enqueue_token<4, 1>(t, p, stream);

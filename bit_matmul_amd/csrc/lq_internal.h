@@ -532,8 +532,9 @@ Int8Plan plan_int8(int64_t B, int64_t N, int64_t K, int cus);
 // partial: Int8Plan::partial_bytes of workspace (unused when ksplit is 1).
 hipError_t launch_int8_gemm(const Int8Gemm& p, const Int8Plan& plan, int* partial, hipStream_t stream);
 hipError_t launch_int8_few(const Int8Gemm& p, const Int8Plan& plan, hipStream_t stream);
-// Rows and product of one token in one launch (t.q, t.scale and p.q, p.scale unused).
-bool int8_token_applies(const QuantRows& t, const Int8Plan& plan);
-hipError_t launch_int8_token(const QuantRows& t, const Int8Gemm& p, hipStream_t stream);
+// Rows and product of one token in one launch (t.q, t.scale and p.q, p.scale
+// unused): the weight rows of a workgroup, 0 where it takes two launches.
+int int8_token_rows(const QuantRows& t, int64_t N, const Int8Plan& plan);
+hipError_t launch_int8_token(const QuantRows& t, const Int8Gemm& p, int rows, hipStream_t stream);
 
 }  // namespace lq

@@ -471,8 +471,11 @@ lq_status lq_int8_gemm_plan(const lq_int8_layer* layer, int64_t B, lq_int8_plan_
 /*
  * The whole 8-bit layer: lq_quant_rows of x with the layer's T, then
  * lq_int8_gemm, the 8-bit rows in the workspace (behind its control area,
- * which is left as it is). Errors: as those two.
+ * which is left as it is). Errors: as those two. lq_int8_linear_plan: how its
+ * product would run, as lq_int8_gemm_plan; tokens is 1 where one token's rows
+ * and product are one launch, whose rows and workgroups it then gives.
  */
+lq_status lq_int8_linear_plan(const lq_int8_layer* layer, int64_t B, lq_int8_plan_info* info);
 lq_status lq_int8_linear_workspace_size(const lq_int8_layer* layer, int64_t B, lq_dtype xtype,
                                         size_t* bytes);
 lq_status lq_int8_linear(const lq_int8_layer* layer, const void* x, lq_dtype xtype, int64_t ldx,
