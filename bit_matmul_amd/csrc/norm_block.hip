@@ -24,8 +24,9 @@ namespace {
 
 // 1 / sqrt(mean(v^2) + eps). Where the sum of squares passes the largest
 // float, v becomes v 2^-80 and the sum is taken again (every thread of the
-// workgroup sees the same sum, so all take the branch together): eps is
-// nothing there, and the norm of v does not change.
+// workgroup sees the same sum, so all take the branch together), with eps
+// 2^-160 (0 below 2^11, which is nothing next to a mean of 4.6e33 or more):
+// the norm of v does not change.
 template <int C>
 __device__ __forceinline__ float inv_rms(float (&v)[C][2][8], int K, float eps, float* red) {
   float s = 0.0f;
@@ -48,7 +49,7 @@ __device__ __forceinline__ float inv_rms(float (&v)[C][2][8], int K, float eps, 
         s = fmaf(v[i][j][k], v[i][j][k], s);
       }
   s = row_reduce<SumF>(s, red + kRowMaxWaves);
-  return 1.0f / sqrtf(s / (float)K);
+  return 1.0f / sqrtf(s / (float)K + eps * 0x1p-80f * 0x1p-80f);
 }
 
 // Each tensor is loaded where it is first used. All loads before the first
