@@ -23,10 +23,12 @@ namespace lq {
 namespace {
 
 // 1 / sqrt(mean(v^2) + eps). Where the sum of squares passes the largest
-// float, v becomes v 2^-80 and the sum is taken again (every thread of the
-// workgroup sees the same sum, so all take the branch together), with eps
-// 2^-160 (0 below 2^11, which is nothing next to a mean of 4.6e33 or more):
-// the norm of v does not change.
+// float, it is taken again of v 2^-80 (every thread of the workgroup sees the
+// same sum, so all take the branch together), with eps 2^-160 (0 below 2^11,
+// which is nothing next to a mean of 4.6e33 or more). The root is then 2^80
+// times too large, and half of that factor goes into v: the norm stays what it
+// is, and neither the root nor a v whose norm is a normal float (8e-22 or more)
+// leaves the normal floats.
 template <int C>
 __device__ __forceinline__ float inv_rms(float (&v)[C][2][8], int K, float eps, float* red) {
   float s = 0.0f;
@@ -45,11 +47,12 @@ __device__ __forceinline__ float inv_rms(float (&v)[C][2][8], int K, float eps, 
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        v[i][j][k] *= 0x1p-80f;
-        s = fmaf(v[i][j][k], v[i][j][k], s);
+        v[i][j][k] *= 0x1p-40f;
+        const float w = v[i][j][k] * 0x1p-40f;
+        s = fmaf(w, w, s);
       }
   s = row_reduce<SumF>(s, red + kRowMaxWaves);
-  return 1.0f / sqrtf(s / (float)K + eps * 0x1p-80f * 0x1p-80f);
+  return 1.0f / sqrtf(s / (float)K + eps * 0x1p-80f * 0x1p-80f) * 0x1p-40f;
 }
 
 // Each tensor is loaded where it is first used. All loads before the first
