@@ -43,3 +43,33 @@ def test_sum_of_squares_in_short_chains(lq, K, lead, post):
     want = 1.0 / np.sqrt(np.mean(h.astype(np.float64) ** 2))
     a = normed(lq, torch.from_numpy(h).to(DEV), post)[h == 1.0]
     assert np.all(np.abs(a / want - 1) <= 3.5 * U32), np.abs(a / want - 1).max() / U32
+
+
+@pytest.mark.parametrize("post", [False, True])
+def test_reciprocal_root_is_rounded_once(lq, post):
+    """Rows of ones and whole numbers m in turn: every sum, and their mean (1 + m^2) / 2, is exact in 32 bits
+    (8 (1 + m^2) in a thread is below 2^24), and eps vanishes in it. The values at the ones are 1 / sqrt of the
+    mean itself: half a unit of the last place, and 2^-16 of that for the correction's own roundings (its
+    residual of at most 2^-22 is off by 2^-45)."""
+    m = np.arange(1, 1400, 2)
+    h = np.ones((len(m), 1024), dtype=np.float32)
+    h[:, 1::2] = m[:, None]
+    a = normed(lq, torch.from_numpy(h).to(DEV), post)[:, 0::2]
+    want = np.sqrt(2.0 / (1.0 + m.astype(np.float64) ** 2))[:, None]
+    ulp = np.spacing(want.astype(np.float32)).astype(np.float64)
+    assert np.all(np.abs(a - want) <= 0.5 * ulp * (1 + 2.0 ** -16)), (np.abs(a - want) / ulp).max()
+
+
+@pytest.mark.parametrize("K", [5, 4099, 40000])
+def test_roots_of_ordinary_rows(lq, K):
+    """The error that a row's values share, at both ends of the range too: the thread's chain of C additions
+    of four chains, 2 joins, 10 levels, halved, and the division's, eps' and the root's roundings."""
+    C = 1 if K <= 16384 else 4
+    bound = ((4 * C + 12) / 2 + 1 + 1) * U32
+    rng = np.random.default_rng(K)
+    for size in (1e-15, 1.0, 1e16):
+        h = torch.from_numpy((rng.standard_normal((8, K)) * size).astype(np.float32)).to(DEV)
+        a = normed(lq, h, False)
+        h64 = host64(h)
+        want = h64 / np.sqrt(np.mean(h64 * h64, axis=1, keepdims=True) + float(np.float32(1e-30)))
+        assert np.all(np.abs(a - want) <= np.abs(want) * (bound + U32))
