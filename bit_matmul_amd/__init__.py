@@ -434,7 +434,8 @@ def lq_int8_gemm_workspace_size(layer: LQInt8Layer, B) -> int:
 
 
 def lq_int8_gemm(layer: LQInt8Layer, q, scale, B, y, ws=None, stream=None) -> None:
-    """y = scale * row_scale * (q w^T) + bias for 8-bit rows q."""
+    """y = scale * row_scale * (q w^T) + bias for 8-bit rows q, which carry the
+    layer's T where it has one (lq_quant_rows'; lq_norm_block's carry none)."""
     qp, ldq = _rows8(q, "q", B, layer.K)
     yp, ldy = _rows(y, "y", B, layer.N)
     wsp, ws_bytes = _here(ws, "ws")
@@ -488,7 +489,9 @@ def lq_norm_block(B, K, y=None, gate=None, act=LQ_ACT_NONE, gate_first=False, po
                   w_post=None, h=None, alpha=1.0, h_out=None, pre=False, w_pre=None,
                   one_plus=False, eps=1e-5, a=None, q=None, scale=None, stream=None) -> None:
     """The norms after and before a block with its gate and scaled residual
-    (lq.h gives the formulas). gate: rows as y, or one vector of K for all."""
+    (lq.h gives the formulas). gate: rows as y, or one vector of K for all.
+    q, scale: 8-bit rows for a layer without T; in front of one with T take the
+    values a to lq_int8_linear."""
     yp = gp = hp = hop = ap = qp = None
     ldy = ldg = ldh = ldho = lda = ldq = yt = ht = at = 0
     if y is not None:

@@ -441,7 +441,9 @@ lq_status lq_quant_rows(const void* x, lq_dtype xtype, int64_t ldx, const void* 
 /*
  * The product of 8-bit rows (lq_quant_rows', lq_norm_block's) with the
  * layer's weights: y, B rows of N in ytype, ldy elements apart. The layer's
- * hb and c are not used. y = (float)sum * (scale * row_scale) + bias in fp32,
+ * hb and c are not used: T is a matter of the rows. For a layer with T they
+ * are lq_quant_rows' with the same hb and c; lq_norm_block's carry no T, and
+ * nothing in them tells (lq_norm_block says what to do there). y = (float)sum * (scale * row_scale) + bias in fp32,
  * rounded once to ytype. ws: device workspace of at least
  * lq_int8_gemm_workspace_size bytes (may be NULL when that size is 0), whose
  * control area is left as it is and whose rest needs no preparation.
@@ -494,7 +496,11 @@ lq_status lq_int8_linear(const lq_int8_layer* layer, const void* x, lq_dtype xty
  *     a  = h' / sqrt(mean(h'^2) + eps) .* w   with LQ_NORM_PRE, w = w_pre
  *                                             (else a = h')
  *
- * a is written as values (a) or as 8-bit rows (q, scale), or both. fp32
+ * a is written as values (a) or as 8-bit rows (q, scale), or both. The 8-bit
+ * rows are those of a itself: they are for a layer without T (hb 1, c NULL).
+ * In front of a layer with T write values and give them to lq_int8_linear (or
+ * to lq_quant_rows with its hb and c, then lq_int8_gemm); channel scales alone
+ * (hb 1) may instead be multiplied into w_pre. fp32
  * throughout; the second norm reads h' before it is rounded to htype.
  * NULL gate: no gate. NULL w: all ones. LQ_NORM_ONE_PLUS: 1 + w in place of
  * w. NULL y: h' = h. NULL h: h' = alpha u. NULL h_out, a, q: not written (one
