@@ -62,9 +62,15 @@ __device__ __forceinline__ TilePlace tile_place(int t, int tiles_n, int tiles_b,
 
 // acc += a c, in place. (The builtin leaves the choice of the result's
 // registers to the compiler: with two steps in a row it took others, and
-// moved and spilled 256 sums. The operands are awaited before an asm as
-// before any use of them; a product follows the last one into the same sum by
-// many others, and acc_ready stands before the sums are read.)
+// moved and spilled 256 sums.) The compiler awaits an asm's operands as before
+// any use of them, but knows no product in it and keeps none of a product's
+// distances. What keeps them: acc_settle and acc_ready stand between a product
+// and whatever else the compiler may do to its sum (moves between the paths
+// that meet behind a loop); a product whose addend and result are the result
+// of the one right before it (the 32 x 32 tile has a single sum) needs no wait
+// at this shape; and operands come from LDS, or are written two instructions
+// earlier. tests/test_mfma_asm.py reads all of it out of the compiled kernels,
+// along every path: a shape of more passes or another compiler shows there.
 __device__ __forceinline__ void mfma_acc(i32x4& acc, i32x4 a, i32x4 c) {
   asm("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(c));
 }
@@ -72,6 +78,10 @@ __device__ __forceinline__ void mfma_zero(i32x4& acc) {
   acc = (i32x4){0, 0, 0, 0};
   asm("" : "+a"(acc));
 }
+// 12 and 32 wait states (a product of 4 passes, this one, takes 8, of 8 passes
+// 12). Without them the compiler moved sums of the 128-row tiles 5 wait states
+// behind their products.
+__device__ __forceinline__ void acc_settle() { asm volatile("s_nop 11" ::: "memory"); }
 __device__ __forceinline__ void acc_ready() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 template <int PN, int PB, int S, int KB>
@@ -262,12 +272,16 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
     do_step(std::integral_constant<int, 1>{}, s + 1);
     if constexpr (S > 2) do_step(std::integral_constant<int, 2>{}, s + 2);
     if constexpr (S > 3) do_step(std::integral_constant<int, 3>{}, s + 3);
+    acc_settle();
   }
-  if (s < steps) do_step(std::integral_constant<int, 0>{}, s);
-  if constexpr (S > 2)
-    if (s + 1 < steps) do_step(std::integral_constant<int, 1>{}, s + 1);
-  if constexpr (S > 3)
-    if (s + 2 < steps) do_step(std::integral_constant<int, 2>{}, s + 2);
+  auto last_step = [&](auto sc, int s) __attribute__((always_inline)) {
+    if (s >= steps) return;
+    do_step(sc, s);
+    acc_settle();
+  };
+  last_step(std::integral_constant<int, 0>{}, s);
+  if constexpr (S > 2) last_step(std::integral_constant<int, 1>{}, s + 1);
+  if constexpr (S > 3) last_step(std::integral_constant<int, 2>{}, s + 2);
 
   // No copy may still be writing LDS when the workgroup ends.
   __builtin_amdgcn_s_waitcnt(0);
