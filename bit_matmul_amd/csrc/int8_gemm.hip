@@ -198,8 +198,7 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
   i32x4 a0[PN], c0[PB], a1[PN], c1[PB];
   __builtin_amdgcn_s_waitcnt(kWaitVm0);
   if (part == s0) zero_past(stage0);
-  __builtin_amdgcn_s_waitcnt(kWaitLds0);
-  __builtin_amdgcn_s_barrier();
+  lds_barrier();
 #pragma unroll
   for (int i = 0; i < PN; ++i) a0[i] = *reinterpret_cast<const i32x4*>(stage0 + rd_a + rd + KB * i);
 #pragma unroll
@@ -257,8 +256,7 @@ __global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void int8_tile_kernel(
     part_step(std::false_type{}, 0u, cur, cur, rd_part(kParts - 1), a0, c0, a1, c1);
     __builtin_amdgcn_s_waitcnt(kWaitVm);
     if (s + 1 == part) zero_past(next);
-    __builtin_amdgcn_s_waitcnt(kWaitLds0);
-    __builtin_amdgcn_s_barrier();
+    lds_barrier();
     part_step(std::true_type{}, lane_at(s + S), cur, next, rd, a1, c1, a0, c0);
   };
   // S steps at a time and one way out of the loop. (The compiler waits for

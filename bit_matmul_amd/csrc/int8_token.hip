@@ -119,9 +119,8 @@ __global__ __launch_bounds__(256) void int8_token_kernel(QuantRows t, Int8Gemm p
 
   // ---- the products
   constexpr int kWaitLds0 = (3 << 14) | (7 << 4) | 15;
-  // All of the codes are written. (A barrier alone: the copies stay in flight.)
-  __builtin_amdgcn_s_waitcnt(kWaitLds0);
-  __builtin_amdgcn_s_barrier();
+  // All of the codes are written, and the copies stay in flight.
+  lds_barrier();
   i32x4 acc[kPanels] = {};
   auto do_step = [&](auto ic, uint4* stage) __attribute__((always_inline)) {
     constexpr int i0 = decltype(ic)::value;

@@ -8,6 +8,17 @@ namespace lq {
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 
+// A barrier for LDS alone (__syncthreads would wait for the copies in flight):
+// this wavefront's accesses are done before it. The builtins say nothing to
+// the compiler about memory: the fences, which are no instructions, keep
+// accesses on their side of it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_s_waitcnt(3 << 14 | 7 << 4 | 15);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Outputs n .. n + 3 (those below N) of token b from their sums, with the
 // token's scale sb, the rows' scales rs and biases. Rows of y need only
 // their element's alignment.
