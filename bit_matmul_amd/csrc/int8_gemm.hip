@@ -405,8 +405,8 @@ static void enqueue_tile(const Int8Gemm& p, const Int8Plan& plan, int* partial, 
 
 // The tiles (stages and bytes per step at the launches below; with `few` those
 // of int8_few.hip, four steps at a time), and what they cost in us, fitted to
-// 2400 measurements over 180 sizes (1 to 2048 tokens, 60 to 200000 outputs, 150
-// to 28672 inputs): a step takes `step` plus `share` for every workgroup on
+// 2500 measurements over 180 sizes (1 to 2048 tokens, 60 to 200000 outputs, 150
+// to 28672 inputs; profiles/int8_product_times.txt): a step takes `step` plus `share` for every workgroup on
 // the compute unit, a workgroup's begin and end take `ends`, and the weights'
 // stream, at the rate that its kernel reaches, hides all but kHidden of that
 // (or is hidden by it). Of these sizes the choice it gives is on average 0.8%

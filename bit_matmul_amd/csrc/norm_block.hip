@@ -15,10 +15,12 @@
 // roundings where its first value is the large one), then a butterfly over
 // lanes and wavefronts.
 //
-// Measured: 2048 rows of 8192 in bf16, both norms and 8-bit rows 27 us (4.4
-// TB/s), in fp32 without 8-bit rows 48 (5.6 TB/s); 777 rows of 4099 in fp32
-// with a gate 17 (3.7); one row 3.4 to 4.8 us (the launch, memory, two
-// reductions). Rows past 32768 (C = 4) spill: 256 of 40000 35 us, 2.3 TB/s.
+// Measured in replays of a graph, tensors from memory (in brackets: the same
+// ones again, from the cache): 2048 rows of 8192 in bf16, both norms and 8-bit
+// rows 30 us (26; 3.9 and 4.6 TB/s), in fp32 without 8-bit rows 53 (43; 5.1 and
+// 6.3); 777 rows of 4099 in fp32 with a gate 20 (16; 3.3 and 4.0); one row 3.8
+// to 5.2 us (the launch, memory, two reductions). Rows past 32768 (C = 4) spill
+// 84 to 92 bytes of scratch a lane: 256 of 40000 37 us (31; 2.2 and 2.6).
 #include "lq_rows.h"
 
 namespace lq {

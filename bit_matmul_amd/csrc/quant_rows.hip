@@ -5,9 +5,21 @@
 //
 // One workgroup per row, the row in registers (lq_rows.h): it is read once,
 // its maximum is one reduction over the workgroup, and the codes are written
-// from the same registers. The time is that of the bytes: 2048 rows of 8192 in
-// bf16 16 us (3.1 TB/s), of 28672 44 (4.0 TB/s), gated 68 (4.3 TB/s); with T
-// 18 and 66. One row of 8192 3.9 us.
+// from the same registers. Without T the time is that of the bytes. Replays of
+// a graph, so that a launch's 3 to 4 us between kernels are in the times, rows
+// from memory: 2048 rows of 8192 in bf16 16 us (3.1 TB/s; the kernel alone, its
+// rows in the cache, 12.4), of 28672 44 (4.0 TB/s), gated 67 (4.4); in fp32 56
+// (5.3 TB/s), gated 130 (4.1). One row of 8192 3.4 us.
+//
+// With T it is not: every row's workgroup reads the channel scales too, which
+// are twice a bf16 row, and 10 butterflies a value stand beside it: 8192 19 us,
+// 28672 66 (2.7 TB/s), gated 115, fp32 85 and gated 189.
+//
+// Registers do not hold everything: of the rows of 16385 to 32768 values (C 2)
+// the fp32 forms with a gate spill (44 bytes of scratch a lane, with T 76), the
+// bf16 form with T a little (12), and the fp32 form with T and without a gate
+// keeps its scales in 41 KB of LDS; past 32768 (C 4) the fp32 form with a gate
+// spills 60 bytes: 256 rows of 40000 32 us (2.9 TB/s), plain bf16 17 (1.9).
 #include <type_traits>
 
 #include "lq_rows.h"
