@@ -70,9 +70,8 @@ PRODUCT_KERNELS = ("sign_fp6_kernel", "sign_fp6_chunked_kernel", "sign_valu_kern
                    "sign_mfma_large_kernel",
                    "wspace_kernel", "decode_fused_kernel", "decode_self_kernel",
                    "decode_split_kernel")
-# The files of the kernels whose HBM traffic the committed summary holds.
 # The source file of each kernel whose traffic the counter summary records
-# (with every header, which they share).
+# (the headers it includes count with it).
 TRAFFIC_SOURCES = {"sign_fp6_kernel": "sign_fp6.hip", "prep_kernel": "prep.hip",
                    "sign_mfma_large_kernel": "sign_mfma.hip", "wspace_kernel": "wspace.hip",
                    "xpw_kernel": "wspace.hip"}
@@ -131,16 +130,24 @@ def parse_args():
 
 def kernel_sources_hash(kernel):
     """Hash of the sources of `kernel` (a key of TRAFFIC_SOURCES): its .hip
-    file and every header. Counters taken on other code are stale for it;
-    host-only files such as the C-ABI dispatch, and the other kernels'
-    files, do not change what it reads or writes."""
+    file and the headers beside it that it includes, directly or through
+    others. Counters taken on other code are stale for it; host-only files
+    such as the C-ABI dispatch, and the other kernels' files and headers, do
+    not change what it reads or writes."""
     import hashlib
+    import re
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "bit_matmul_amd", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name.endswith(".h") or name == TRAFFIC_SOURCES[kernel]:
-            with open(os.path.join(csrc, name), "rb") as f:
-                h.update(name.encode() + b"\0" + f.read())
+    texts, todo = {}, [TRAFFIC_SOURCES[kernel]]
+    while todo:
+        name = todo.pop()
+        path = os.path.join(csrc, name)
+        if name not in texts and os.path.exists(path):
+            with open(path, "rb") as f:
+                texts[name] = f.read()
+            todo += [m.decode() for m in re.findall(rb'^#include "([^"/]+)"', texts[name], re.M)]
+    for name in sorted(texts):
+        h.update(name.encode() + b"\0" + texts[name])
     return h.hexdigest()[:16]
 
 

@@ -12,6 +12,7 @@
 #include <mutex>
 #include <vector>
 
+#include "lq_8bit.h"
 #include "lq_internal.h"
 
 namespace lq {

@@ -2,7 +2,7 @@
 // int8_token.hip).
 #pragma once
 
-#include "lq_internal.h"
+#include "lq_8bit.h"
 
 namespace lq {
 

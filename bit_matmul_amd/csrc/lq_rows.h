@@ -10,7 +10,7 @@
 // needs no LDS.
 #pragma once
 
-#include "lq_internal.h"
+#include "lq_8bit.h"
 #include "lq_prep.h"
 
 namespace lq {
