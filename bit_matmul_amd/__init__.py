@@ -22,7 +22,9 @@ from ._lib import (LQ_MULTI_MAX, LQ_ENCODE_MAX_D, LQ_ENCODE_MAX_SMALL_D, LQ_ENCO
                    LQ_WS_ERROR_WORD, LQ_NOALLOC_SCRATCH_BYTES, LQ_ERR_DEVICE, LQ_MAX_L, LQError,
                    LQLayer, LQPlanInfo, LQInt8Layer, LQInt8PlanInfo, LQNormBlockArgs, LQ_ACT_NONE, LQ_ACT_SILU,
                    LQ_ACT_GELU, LQ_ACT_SIGMOID, LQ_ACT_TANH, LQ_NORM_POST, LQ_NORM_PRE,
-                   LQ_NORM_GATE_FIRST, LQ_NORM_ONE_PLUS, LQ_ROW_MAX_K, LQ_INT8_MAX_K, LQ_INT8_MAX_LD)
+                   LQ_NORM_GATE_FIRST, LQ_NORM_ONE_PLUS, LQ_ROW_MAX_K, LQ_INT8_MAX_K, LQ_INT8_MAX_LD,
+                   LQMx4Layer, LQMx4PlanInfo, LQQkNormRopeArgs, LQ_MX4_MAX_K, LQ_QK_MAX_DIM, LQ_QK_NORM,
+                   LQ_QK_ONE_PLUS, LQ_QK_INTERLEAVED)
 
 __all__ = [
     "lq_version", "lq_packed_size", "lq_pack_signs", "lq_unpack_signs", "lq_hadamard_scale",
@@ -45,6 +47,10 @@ __all__ = [
     "LQNormBlockArgs", "LQ_ACT_NONE", "LQ_ACT_SILU", "LQ_ACT_GELU", "LQ_ACT_SIGMOID",
     "LQ_ACT_TANH", "LQ_NORM_POST", "LQ_NORM_PRE", "LQ_NORM_GATE_FIRST", "LQ_NORM_ONE_PLUS",
     "LQ_ROW_MAX_K", "LQ_INT8_MAX_K", "LQ_INT8_MAX_LD",
+    "lq_mx4_scale_size", "lq_mx4_quant_rows", "mx4_layer_struct", "lq_mx4_gemm_workspace_size",
+    "lq_mx4_gemm", "lq_mx4_gemm_plan", "lq_mx4_linear_workspace_size", "lq_mx4_linear",
+    "lq_qk_norm_rope", "LQMx4Layer", "LQMx4PlanInfo", "LQQkNormRopeArgs", "LQ_MX4_MAX_K",
+    "LQ_QK_MAX_DIM", "LQ_QK_NORM", "LQ_QK_ONE_PLUS", "LQ_QK_INTERLEAVED",
 ]
 
 _DTYPES = {torch.float32: LQ_F32, torch.bfloat16: LQ_BF16}
@@ -526,3 +532,179 @@ def lq_norm_block(B, K, y=None, gate=None, act=LQ_ACT_NONE, gate_first=False, po
                               _vec(w_pre, "w_pre", K) or 0, ap or 0, qp or 0, _vec(scale, "scale", B) or 0,
                               ldy, ldg, ldh, ldho, lda, ldq, yt, ht, at, act, alpha, eps, flags, 0)
     _check(_NORM_BLOCK(p, _stream(stream)), "lq_norm_block")
+
+
+def _rows4(t, name: str, B: int, K: int):
+    """_rows of 4-bit rows: bytes of two codes, 16 for each 32 values."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+        raise ValueError(f"{name} must be a uint8 tensor")
+    width = 16 * -(-K // 32)
+    ptr, ld = _rows(t, name, B, width)
+    if t.size(0) == 1:
+        ld = max(width, (ld + 15) & -16)
+    return ptr, ld
+
+
+def _scales4(t, name: str, rows: int, K: int):
+    """The address of the scales of 4-bit rows."""
+    need = -(-rows // 16) * -(-K // 256) * 128
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.numel() < need:
+        raise ValueError(f"{name} must be a uint8 tensor of {need} bytes")
+    return _here(t, name)[0]
+
+
+def lq_mx4_scale_size(rows, K) -> int:
+    """Bytes of the scales of `rows` 4-bit rows of K values."""
+    out = ctypes.c_size_t()
+    _check(_lib.LIB.lq_mx4_scale_size(rows, K, ctypes.byref(out)), "lq_mx4_scale_size")
+    return out.value
+
+
+def lq_mx4_quant_rows(x, B, K, q, scale, gate=None, act=LQ_ACT_NONE, hb=1, c=None, stream=None) -> None:
+    """4-bit rows q (uint8, 16 bytes for each 32 values) and their scales
+    (uint8, lq_mx4_scale_size(B, K) bytes in the library's panels) of
+    T (act(gate) * x); x and gate: 2-D, of one dtype. Weights take the same
+    way."""
+    xt = _dtype(x, "x")
+    xp, ldx = _rows(x, "x", B, K)
+    gp, ldg = _gate(gate, x, B, K)
+    qp, ldq = _rows4(q, "q", B, K)
+    _check(_lib.LIB.lq_mx4_quant_rows(xp, xt, ldx, gp, ldg, act, B, K, hb, _vec(c, "c", K), qp, ldq,
+                                      _scales4(scale, "scale", B, K), _stream(stream)),
+           "lq_mx4_quant_rows")
+
+
+def _gate(gate, x, B, K):
+    if gate is None:
+        return None, 0
+    if gate.dtype != x.dtype:
+        raise ValueError("gate must have x's dtype")
+    return _rows(gate, "gate", B, K)
+
+
+def mx4_layer_struct(N, K, w, w_scale, row_scale=None, hb=1, c=None, bias=None) -> LQMx4Layer:
+    """Fill a ``struct lq_mx4_layer`` from device tensors (the caller keeps
+    the tensors alive while the struct is used); w, w_scale: uint8, N rows of K
+    codes and their scales, as lq_mx4_quant_rows writes them."""
+    wp, ldw = _rows4(w, "w", N, K)
+    layer = LQMx4Layer(N, K, ldw, hb, 0, wp, _scales4(w_scale, "w_scale", N, K), _vec(c, "c", K),
+                       _vec(row_scale, "row_scale", N), _vec(bias, "bias", N))
+    layer.device = w.get_device()
+    return layer
+
+
+def lq_mx4_gemm_workspace_size(layer: LQMx4Layer, B) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.LIB.lq_mx4_gemm_workspace_size(ctypes.byref(layer), B, ctypes.byref(out)),
+           "lq_mx4_gemm_workspace_size")
+    return out.value
+
+
+def lq_mx4_gemm(layer: LQMx4Layer, q, scale, B, y, ws=None, stream=None) -> None:
+    """y = row_scale * (q w^T) + bias for 4-bit rows q, which carry the layer's
+    T where it has one."""
+    qp, ldq = _rows4(q, "q", B, layer.K)
+    yp, ldy = _rows(y, "y", B, layer.N)
+    wsp, ws_bytes = _here(ws, "ws")
+    _layer_here(layer)
+    _check(_lib.LIB.lq_mx4_gemm(ctypes.byref(layer), qp, ldq, _scales4(scale, "scale", B, layer.K), B, yp,
+                                _dtype(y, "y"), ldy, wsp, ws_bytes, _stream(stream)), "lq_mx4_gemm")
+
+
+def lq_mx4_gemm_plan(layer: LQMx4Layer, B) -> dict:
+    """Tile and split of the reduction that lq_mx4_gemm would use."""
+    info = LQMx4PlanInfo()
+    _check(_lib.LIB.lq_mx4_gemm_plan(ctypes.byref(layer), B, ctypes.byref(info)), "lq_mx4_gemm_plan")
+    return {f: getattr(info, f) for f, _ in LQMx4PlanInfo._fields_}
+
+
+def lq_mx4_linear_workspace_size(layer: LQMx4Layer, B, xtype) -> int:
+    out = ctypes.c_size_t()
+    xt = _DTYPES[xtype] if isinstance(xtype, torch.dtype) else int(xtype)
+    _check(_lib.LIB.lq_mx4_linear_workspace_size(ctypes.byref(layer), B, xt, ctypes.byref(out)),
+           "lq_mx4_linear_workspace_size")
+    return out.value
+
+
+def lq_mx4_linear(layer: LQMx4Layer, x, B, y, ws=None, gate=None, act=LQ_ACT_NONE, stream=None) -> None:
+    """The whole 4-bit layer of act(gate) * x: 4-bit rows, then the product."""
+    xp, ldx = _rows(x, "x", B, layer.K)
+    gp, ldg = _gate(gate, x, B, layer.K)
+    yp, ldy = _rows(y, "y", B, layer.N)
+    wsp, ws_bytes = _here(ws, "ws")
+    _layer_here(layer)
+    _check(_lib.LIB.lq_mx4_linear(ctypes.byref(layer), xp, _dtype(x, "x"), ldx, gp, ldg, act, B, yp,
+                                  _dtype(y, "y"), ldy, wsp, ws_bytes, _stream(stream)),
+           "lq_mx4_linear")
+
+
+def _head_rows(t, name: str, B: int, heads: int, dim: int):
+    """(address, token stride, head stride) of a GPU tensor (tokens, heads, dim)
+    whose heads are dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a GPU tensor of three dimensions")
+    if t.shape[0] < B or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, ({B}, {heads}, {dim}) is needed")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    ld, ld_head, step = t.stride()
+    if step != 1 and dim > 1:
+        raise ValueError(f"{name}'s heads must be dense")
+    return t.data_ptr(), ld, ld_head
+
+
+_QK_ARGS = struct.Struct("q4Q8q4Q6ifIQ")
+assert _QK_ARGS.size == ctypes.sizeof(LQQkNormRopeArgs)
+_QK_NORM_ROPE = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, ctypes.c_void_p)(("lq_qk_norm_rope", _lib.LIB))
+_POS_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def lq_qk_norm_rope(pos, freq, q=None, k=None, q_out=None, k_out=None, norm=True, w_q=None, w_k=None,
+                    one_plus=False, eps=1e-5, interleaved=False, stream=None) -> None:
+    """Norms of queries and keys for each head and the rotation by position
+    (lq.h gives the formulas). q, k and their outputs: (tokens, heads, dim) of
+    one dtype, any token and head strides; an output may be its input. pos: int32 or int64, one for
+    each token; freq: float64, an angle a position for each pair of values (2 of
+    them for each: the first 2 * freq.numel() of a head are rotated)."""
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q or k is needed")
+    dt = _dtype(some, "q" if q is not None else "k")
+    if some.dim() != 3:
+        raise ValueError("q and k must be GPU tensors of three dimensions")
+    B, _, dim = some.shape
+    ptrs, lds, heads = [], [], []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            ptrs += [0, 0]
+            lds += [0, 0, 0, 0]
+            heads.append(0)
+            continue
+        if out is None or x.dtype != some.dtype or out.dtype != some.dtype:
+            raise ValueError(f"{name} and {name}_out must be given, of one dtype")
+        n = x.shape[1] if x.dim() == 3 else 0
+        if x.dim() == 3 and x.shape[0] != B:
+            raise ValueError("q and k must have the same tokens")
+        xp, ld, ldh = _head_rows(x, name, B, n, dim)
+        op, ldo, ldoh = _head_rows(out, name + "_out", B, n, dim)
+        ptrs += [xp, op]
+        lds += [ld, ldh, ldo, ldoh]
+        heads.append(n)
+    rot = 0 if freq is None else 2 * freq.numel()
+    pp = fp = 0
+    width = 8
+    if rot:
+        width = _POS_BYTES.get(pos.dtype)
+        if width is None or freq.dtype != torch.float64:
+            raise ValueError("pos must be int32 or int64 and freq float64")
+        if pos.numel() < B:
+            raise ValueError(f"pos must hold {B} positions")
+        pp, fp = _here(pos, "pos")[0], _here(freq, "freq")[0]
+    flags = ((LQ_QK_NORM if norm else 0) | (LQ_QK_ONE_PLUS if one_plus else 0) |
+             (LQ_QK_INTERLEAVED if interleaved else 0))
+    p = _QK_ARGS.pack(B, ptrs[0], ptrs[2], ptrs[1], ptrs[3], lds[0], lds[1], lds[4], lds[5], lds[2], lds[3], lds[6],
+                      lds[7], _vec(w_q, "w_q", dim) or 0, _vec(w_k, "w_k", dim) or 0, pp, fp, *heads, dim, rot, dt,
+                      width, eps, flags, 0)
+    _check(_QK_NORM_ROPE(p, _stream(stream)), "lq_qk_norm_rope")

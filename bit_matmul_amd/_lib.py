@@ -2,7 +2,7 @@
 from __future__ import annotations
 
 import ctypes
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().parent / "liblq.so"
@@ -27,6 +27,9 @@ LQ_ROW_MAX_K = 65536
 LQ_INT8_MAX_K = 131071
 LQ_INT8_MAX_LD = 1 << 23
 LQ_NOALLOC_SCRATCH_BYTES = 16 << 20
+LQ_MX4_MAX_K = 1 << 20
+LQ_QK_MAX_DIM = 512
+LQ_QK_NORM, LQ_QK_ONE_PLUS, LQ_QK_INTERLEAVED = 1, 2, 4
 
 # Every symbol include/lq.h declares.
 EXPORTS = [
@@ -41,6 +44,8 @@ EXPORTS = [
     "lq_encode_pinv", "lq_quant_rows", "lq_int8_gemm_workspace_size", "lq_int8_gemm",
     "lq_int8_linear_workspace_size", "lq_int8_linear", "lq_norm_block",
     "lq_int8_gemm_plan", "lq_int8_linear_plan",
+    "lq_mx4_scale_size", "lq_mx4_quant_rows", "lq_mx4_gemm_workspace_size", "lq_mx4_gemm",
+    "lq_mx4_gemm_plan", "lq_mx4_linear_workspace_size", "lq_mx4_linear", "lq_qk_norm_rope",
 ]
 
 
@@ -85,6 +90,35 @@ class LQNormBlockArgs(ctypes.Structure):
         ("lda", c_int64), ("ldq", c_int64),
         ("ytype", c_int32), ("htype", c_int32), ("atype", c_int32), ("act", c_int32),
         ("alpha", c_float), ("eps", c_float), ("flags", c_uint32), ("reserved", c_uint32),
+    ]
+
+
+class LQMx4Layer(ctypes.Structure):
+    """Mirror of ``struct lq_mx4_layer``."""
+    _fields_ = [
+        ("N", c_int64), ("K", c_int64), ("ldw", c_int64), ("hb", c_int32), ("reserved", c_int32),
+        ("w", c_void_p), ("w_scale", c_void_p), ("c", c_void_p), ("row_scale", c_void_p),
+        ("bias", c_void_p),
+    ]
+
+
+class LQMx4PlanInfo(ctypes.Structure):
+    """Mirror of ``struct lq_mx4_plan_info``."""
+    _fields_ = [("rows", c_int32), ("tokens", c_int32), ("ksplit", c_int32), ("workgroups", c_int32)]
+
+
+class LQQkNormRopeArgs(ctypes.Structure):
+    """Mirror of ``struct lq_qk_norm_rope_args``."""
+    _fields_ = [
+        ("B", c_int64),
+        ("q", c_void_p), ("k", c_void_p), ("q_out", c_void_p), ("k_out", c_void_p),
+        ("ldq", c_int64), ("ldq_head", c_int64), ("ldk", c_int64), ("ldk_head", c_int64),
+        ("ldq_out", c_int64), ("ldq_out_head", c_int64), ("ldk_out", c_int64),
+        ("ldk_out_head", c_int64),
+        ("w_q", c_void_p), ("w_k", c_void_p), ("pos", c_void_p), ("freq", c_void_p),
+        ("q_heads", c_int32), ("k_heads", c_int32), ("dim", c_int32), ("rot", c_int32),
+        ("dtype", c_int32), ("pos_bytes", c_int32), ("eps", c_float), ("flags", c_uint32),
+        ("reserved", c_uint64),
     ]
 
 
@@ -148,6 +182,17 @@ def _load():
         "lq_int8_gemm_plan": (c_int, [POINTER(LQInt8Layer), i64, POINTER(LQInt8PlanInfo)]),
         "lq_int8_linear_plan": (c_int, [POINTER(LQInt8Layer), i64, POINTER(LQInt8PlanInfo)]),
         "lq_norm_block": (c_int, [POINTER(LQNormBlockArgs), vp]),
+        "lq_mx4_scale_size": (c_int, [i64, i64, POINTER(sz)]),
+        "lq_mx4_quant_rows": (c_int, [vp, c_int, i64, vp, i64, c_int, i64, i64, i32, vp, vp, i64,
+                                      vp, vp]),
+        "lq_mx4_gemm_workspace_size": (c_int, [POINTER(LQMx4Layer), i64, POINTER(sz)]),
+        "lq_mx4_gemm": (c_int, [POINTER(LQMx4Layer), vp, i64, vp, i64, vp, c_int, i64, vp, sz,
+                                vp]),
+        "lq_mx4_gemm_plan": (c_int, [POINTER(LQMx4Layer), i64, POINTER(LQMx4PlanInfo)]),
+        "lq_mx4_linear_workspace_size": (c_int, [POINTER(LQMx4Layer), i64, c_int, POINTER(sz)]),
+        "lq_mx4_linear": (c_int, [POINTER(LQMx4Layer), vp, c_int, i64, vp, i64, c_int, i64, vp,
+                                  c_int, i64, vp, sz, vp]),
+        "lq_qk_norm_rope": (c_int, [POINTER(LQQkNormRopeArgs), vp]),
     }
     for name, (res, args) in protos.items():
         fn = getattr(lib, name)

@@ -13,6 +13,8 @@
 #include <vector>
 
 #include "lq_8bit.h"
+#include "lq_mx4.h"
+#include "lq_qk.h"
 #include "lq_internal.h"
 
 namespace lq {
@@ -1045,7 +1047,8 @@ Int8Ws int8_ws(const lq_int8_layer* l, int64_t B) {
   return w;
 }
 
-void fill_hb(lq::QuantRows* p, int32_t hb) {
+template <typename Rows>
+void fill_hb(Rows* p, int32_t hb) {
   p->lhb = 0;
   while ((1 << p->lhb) < hb) ++p->lhb;
   // 1/sqrt(hb) for hb = 2^k: exact when k is even, correctly rounded otherwise.
@@ -1213,6 +1216,250 @@ lq_status lq_norm_block(const lq_norm_block_args* a, void* stream) {
                         post, pre, (a->flags & LQ_NORM_GATE_FIRST) != 0,
                         (a->flags & LQ_NORM_ONE_PLUS) != 0};
   return hip_status(lq::launch_norm_block(p, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- microscaled 4-bit layers
+
+static_assert(LQ_QK_MAX_DIM == lq::kQkMaxDim, "heads' limit");
+
+namespace {
+
+lq_status check_rows4(const uint8_t* q, int64_t ldq, int64_t K) {
+  if (!aligned16(q) || ldq % 16 != 0) return LQ_ERR_INVALID_ARG;
+  if (ldq > LQ_INT8_MAX_LD) return LQ_ERR_UNSUPPORTED;
+  return check_ld(ldq, lq::mx4_row_bytes(K));
+}
+
+lq_status check_mx4_layer(const lq_mx4_layer* l, int64_t B) {
+  if (l == nullptr || l->reserved != 0 || l->N < 0) return LQ_ERR_INVALID_ARG;
+  if (l->N > kMaxInt8N) return LQ_ERR_UNSUPPORTED;
+  lq_status s = check_rows(B, l->K, LQ_MX4_MAX_K);
+  if (s == LQ_OK) s = check_hb(l->K, l->hb);
+  if (s == LQ_OK && l->ldw % 16 != 0) s = LQ_ERR_INVALID_ARG;
+  if (s == LQ_OK) s = check_ld(l->ldw, lq::mx4_row_bytes(l->K));
+  if (s == LQ_OK && (l->ldw > LQ_INT8_MAX_LD || !mul_ok(B, l->N, kMaxInt8Out))) s = LQ_ERR_UNSUPPORTED;
+  return s;
+}
+
+lq_status check_mx4_ptrs(const lq_mx4_layer* l, const void* y, lq_dtype ytype, int64_t ldy) {
+  if (!valid_dtype(ytype) || !aligned_to(y, ytype)) return LQ_ERR_INVALID_ARG;
+  if (!aligned16(l->w) || !aligned16(l->w_scale)) return LQ_ERR_INVALID_ARG;
+  if (l->row_scale != nullptr && !aligned_to(l->row_scale, LQ_F32)) return LQ_ERR_INVALID_ARG;
+  if (l->bias != nullptr && !aligned_to(l->bias, LQ_F32)) return LQ_ERR_INVALID_ARG;
+  return check_ld(ldy, l->N);
+}
+
+lq::Mx4Plan mx4_plan(const lq_mx4_layer* l, int64_t B) {
+  return lq::plan_mx4(B, l->N, l->K, device_cus());
+}
+size_t mx4_gemm_bytes(const lq::Mx4Plan& plan) {
+  return plan.ksplit > 1 ? align_up(lq::kControlBytes) + align_up(plan.partial_bytes) : 0;
+}
+float* mx4_partial(const lq::Mx4Plan& plan, void* ws, size_t off) {
+  return plan.ksplit > 1 ? reinterpret_cast<float*>(static_cast<char*>(ws) + off) : nullptr;
+}
+
+// The pieces of lq_mx4_linear's workspace, behind the control area.
+struct Mx4Ws {
+  lq::Mx4Plan plan;
+  size_t off_q, off_scale, off_partial, total;
+  int64_t ldq;
+};
+Mx4Ws mx4_ws(const lq_mx4_layer* l, int64_t B) {
+  Mx4Ws w;
+  w.plan = mx4_plan(l, B);
+  w.ldq = (lq::mx4_row_bytes(l->K) + 127) & ~int64_t(127);     // whole cache lines, as int8_ws
+  w.off_q = align_up(lq::kControlBytes);
+  w.off_scale = w.off_q + align_up((size_t)B * w.ldq);
+  w.off_partial = w.off_scale + align_up((size_t)lq::mx4_scale_bytes(B, l->K));
+  w.total = w.off_partial + align_up(w.plan.partial_bytes);
+  return w;
+}
+
+lq::Mx4Gemm mx4_args(const lq_mx4_layer* l, const uint8_t* q, int64_t ldq, const uint8_t* scale,
+                     int64_t B, void* y, lq_dtype ytype, int64_t ldy) {
+  return {q, scale, l->w, l->w_scale, l->row_scale, l->bias, y, B, l->N, l->K, ldq, l->ldw, ldy,
+          ytype == LQ_BF16};
+}
+
+// x, gate and c of 4-bit rows.
+lq_status check_row_inputs(const void* x, lq_dtype xtype, int64_t ldx, const void* gate, int64_t ldg,
+                           const float* c, int64_t K) {
+  lq_status s = check_ld(ldx, K);
+  if (s == LQ_OK && gate != nullptr) s = check_ld(ldg, K);
+  if (s != LQ_OK) return s;
+  if (!aligned_to(x, xtype) || (gate != nullptr && !aligned_to(gate, xtype))) return LQ_ERR_INVALID_ARG;
+  return c == nullptr || aligned_to(c, LQ_F32) ? LQ_OK : LQ_ERR_INVALID_ARG;
+}
+
+lq::Mx4Rows mx4_row_args(const void* x, lq_dtype xtype, int64_t ldx, const void* gate, int64_t ldg,
+                         lq_act act, int64_t B, int64_t K, int32_t hb, const float* c, uint8_t* q,
+                         int64_t ldq, uint8_t* scale) {
+  lq::Mx4Rows p{x, gate, c, q, scale, B, K, ldx, ldg, ldq, (int)act, 0, 1.0f, xtype == LQ_BF16};
+  fill_hb(&p, hb);
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+lq_status lq_mx4_scale_size(int64_t rows, int64_t K, size_t* bytes) {
+  if (bytes == nullptr || rows < 0 || K < 1) return LQ_ERR_INVALID_ARG;
+  if (rows > kMaxInt8N || K > LQ_MX4_MAX_K) return LQ_ERR_UNSUPPORTED;
+  *bytes = (size_t)lq::mx4_scale_bytes(rows, K);
+  return LQ_OK;
+}
+
+lq_status lq_mx4_quant_rows(const void* x, lq_dtype xtype, int64_t ldx, const void* gate, int64_t ldg,
+                            lq_act act, int64_t B, int64_t K, int32_t hb, const float* c, uint8_t* q,
+                            int64_t ldq, uint8_t* scale, void* stream) {
+  if (!valid_dtype(xtype) || !valid_act(act)) return LQ_ERR_INVALID_ARG;
+  if (B < 0 || K < 1) return LQ_ERR_INVALID_ARG;
+  // (rows of weights too: as many as a layer has)
+  if (B > kMaxInt8N || K > LQ_MX4_MAX_K) return LQ_ERR_UNSUPPORTED;
+  lq_status s = check_hb(K, hb);
+  if (s != LQ_OK) return s;
+  if (B == 0) return LQ_OK;
+  s = check_row_inputs(x, xtype, ldx, gate, ldg, c, K);
+  if (s == LQ_OK) s = check_rows4(q, ldq, K);
+  if (s == LQ_OK && !aligned16(scale)) s = LQ_ERR_INVALID_ARG;
+  if (s != LQ_OK) return s;
+  return hip_status(lq::launch_mx4_rows(
+      mx4_row_args(x, xtype, ldx, gate, ldg, act, B, K, hb, c, q, ldq, scale), (hipStream_t)stream));
+}
+
+lq_status lq_mx4_gemm_workspace_size(const lq_mx4_layer* layer, int64_t B, size_t* bytes) {
+  if (bytes == nullptr) return LQ_ERR_INVALID_ARG;
+  lq_status s = check_mx4_layer(layer, B);
+  if (s != LQ_OK) return s;
+  *bytes = B == 0 || layer->N == 0 ? 0 : mx4_gemm_bytes(mx4_plan(layer, B));
+  return LQ_OK;
+}
+
+lq_status lq_mx4_gemm_plan(const lq_mx4_layer* layer, int64_t B, lq_mx4_plan_info* info) {
+  if (info == nullptr) return LQ_ERR_INVALID_ARG;
+  lq_status s = check_mx4_layer(layer, B);
+  if (s != LQ_OK) return s;
+  if (B < 1 || layer->N < 1) return LQ_ERR_INVALID_ARG;
+  const lq::Mx4Plan p = mx4_plan(layer, B);
+  *info = {p.rows, p.tokens, p.ksplit, p.tiles * p.ksplit};
+  return LQ_OK;
+}
+
+lq_status lq_mx4_gemm(const lq_mx4_layer* layer, const uint8_t* q, int64_t ldq,
+                      const uint8_t* scale, int64_t B, void* y, lq_dtype ytype, int64_t ldy,
+                      void* ws, size_t ws_bytes, void* stream) {
+  lq_status s = check_mx4_layer(layer, B);
+  if (s != LQ_OK) return s;
+  if (B == 0 || layer->N == 0) return LQ_OK;
+  const lq::Mx4Plan plan = mx4_plan(layer, B);
+  s = check_mx4_ptrs(layer, y, ytype, ldy);
+  if (s == LQ_OK && !aligned16(scale)) s = LQ_ERR_INVALID_ARG;
+  if (s == LQ_OK) s = check_rows4(q, ldq, layer->K);
+  if (s == LQ_OK) s = check_ws(ws, ws_bytes, mx4_gemm_bytes(plan));
+  if (s != LQ_OK) return s;
+  return hip_status(lq::launch_mx4_gemm(mx4_args(layer, q, ldq, scale, B, y, ytype, ldy), plan,
+                                        mx4_partial(plan, ws, align_up(lq::kControlBytes)),
+                                        (hipStream_t)stream));
+}
+
+lq_status lq_mx4_linear_workspace_size(const lq_mx4_layer* layer, int64_t B, lq_dtype xtype,
+                                       size_t* bytes) {
+  if (bytes == nullptr || !valid_dtype(xtype)) return LQ_ERR_INVALID_ARG;
+  lq_status s = check_mx4_layer(layer, B);
+  if (s != LQ_OK) return s;
+  *bytes = B == 0 || layer->N == 0 ? 0 : mx4_ws(layer, B).total;
+  return LQ_OK;
+}
+
+lq_status lq_mx4_linear(const lq_mx4_layer* layer, const void* x, lq_dtype xtype, int64_t ldx,
+                        const void* gate, int64_t ldg, lq_act act, int64_t B, void* y,
+                        lq_dtype ytype, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_dtype(xtype) || !valid_act(act)) return LQ_ERR_INVALID_ARG;
+  lq_status s = check_mx4_layer(layer, B);
+  if (s != LQ_OK) return s;
+  if (B == 0 || layer->N == 0) return LQ_OK;
+  const Mx4Ws w = mx4_ws(layer, B);
+  s = check_row_inputs(x, xtype, ldx, gate, ldg, layer->c, layer->K);
+  if (s == LQ_OK) s = check_mx4_ptrs(layer, y, ytype, ldy);
+  if (s == LQ_OK) s = check_ws(ws, ws_bytes, w.total);
+  if (s != LQ_OK) return s;
+  char* base = static_cast<char*>(ws);
+  uint8_t* q = reinterpret_cast<uint8_t*>(base + w.off_q);
+  uint8_t* scale = reinterpret_cast<uint8_t*>(base + w.off_scale);
+  s = hip_status(lq::launch_mx4_rows(mx4_row_args(x, xtype, ldx, gate, ldg, act, B, layer->K, layer->hb,
+                                                  layer->c, q, w.ldq, scale), (hipStream_t)stream));
+  if (s != LQ_OK) return s;
+  return hip_status(lq::launch_mx4_gemm(mx4_args(layer, q, w.ldq, scale, B, y, ytype, ldy), w.plan,
+                                        mx4_partial(w.plan, ws, w.off_partial), (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- norm and rotation of heads
+
+namespace {
+
+constexpr int64_t kMaxHeadLd = int64_t(1) << 40;
+
+// `inner` and `outer` strides of `ni` and `no` runs of dim elements: apart.
+bool runs_apart(int64_t inner, int64_t ni, int64_t outer, int64_t no, int64_t dim) {
+  if (ni > 1 && inner < dim) return false;
+  const int64_t span = ni > 1 ? (ni - 1) * inner + dim : dim;
+  return no <= 1 || outer >= span;
+}
+
+lq_status check_heads(const void* x, const void* out, int64_t ld, int64_t ldh, int64_t ldo, int64_t ldoh,
+                      int64_t B, int32_t heads, int32_t dim, lq_dtype t) {
+  if (heads < 0 || (heads == 0) != (x == nullptr) || (x == nullptr) != (out == nullptr)) return LQ_ERR_INVALID_ARG;
+  if (heads > (1 << 16)) return LQ_ERR_UNSUPPORTED;
+  if (heads == 0) return LQ_OK;
+  if (!aligned_to(x, t) || !aligned_to(out, t)) return LQ_ERR_INVALID_ARG;
+  for (int64_t v : {ld, ldh, ldo, ldoh}) {
+    if (v < 0) return LQ_ERR_INVALID_ARG;
+    if (v > kMaxHeadLd) return LQ_ERR_UNSUPPORTED;
+  }
+  if (!runs_apart(ldoh, heads, ldo, B, dim) && !runs_apart(ldo, B, ldoh, heads, dim)) return LQ_ERR_INVALID_ARG;
+  if (x == out && ((B > 1 && ld != ldo) || (heads > 1 && ldh != ldoh))) return LQ_ERR_INVALID_ARG;
+  return LQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lq_status lq_qk_norm_rope(const lq_qk_norm_rope_args* a, void* stream) {
+  if (a == nullptr || a->reserved != 0) return LQ_ERR_INVALID_ARG;
+  constexpr uint32_t kFlags = LQ_QK_NORM | LQ_QK_ONE_PLUS | LQ_QK_INTERLEAVED;
+  const lq_dtype t = (lq_dtype)a->dtype;
+  if ((a->flags & ~kFlags) != 0 || !valid_dtype(t)) return LQ_ERR_INVALID_ARG;
+  const bool norm = a->flags & LQ_QK_NORM;
+  if (norm && !(a->eps > 0.0f && std::isnormal(a->eps))) return LQ_ERR_INVALID_ARG;
+  if (a->B < 0 || a->dim < 1 || a->rot < 0 || a->rot > a->dim || a->rot % 2 != 0) return LQ_ERR_INVALID_ARG;
+  if (a->B > kMaxBatch || a->dim > LQ_QK_MAX_DIM) return LQ_ERR_UNSUPPORTED;
+  if (a->B == 0) return LQ_OK;
+  lq_status s = check_heads(a->q, a->q_out, a->ldq, a->ldq_head, a->ldq_out, a->ldq_out_head, a->B, a->q_heads,
+                            a->dim, t);
+  if (s == LQ_OK)
+    s = check_heads(a->k, a->k_out, a->ldk, a->ldk_head, a->ldk_out, a->ldk_out_head, a->B, a->k_heads, a->dim, t);
+  if (s != LQ_OK) return s;
+  if (a->q == nullptr && a->k == nullptr) return LQ_ERR_INVALID_ARG;
+  if ((a->w_q != nullptr && !aligned_to(a->w_q, LQ_F32)) || (a->w_k != nullptr && !aligned_to(a->w_k, LQ_F32)))
+    return LQ_ERR_INVALID_ARG;
+  if (a->rot > 0) {
+    if (a->pos_bytes != 4 && a->pos_bytes != 8) return LQ_ERR_INVALID_ARG;
+    if (a->pos == nullptr || reinterpret_cast<uintptr_t>(a->pos) % (uintptr_t)a->pos_bytes != 0) return LQ_ERR_INVALID_ARG;
+    if (a->freq == nullptr || reinterpret_cast<uintptr_t>(a->freq) % 8 != 0) return LQ_ERR_INVALID_ARG;
+  }
+  const lq::QkNormRope p{
+      {{a->q, a->q_out, a->w_q, a->ldq, a->ldq_head, a->ldq_out, a->ldq_out_head, a->q_heads},
+       {a->k, a->k_out, a->w_k, a->ldk, a->ldk_head, a->ldk_out, a->ldk_out_head, a->k_heads}},
+      a->pos, a->freq, a->B, a->dim, a->rot, a->eps, t == LQ_BF16, a->pos_bytes == 8, norm,
+      (a->flags & LQ_QK_ONE_PLUS) != 0, (a->flags & LQ_QK_INTERLEAVED) != 0};
+  return hip_status(lq::launch_qk_norm_rope(p, (hipStream_t)stream));
 }
 
 }  // extern "C"

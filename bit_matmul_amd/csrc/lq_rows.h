@@ -1,4 +1,4 @@
-// Device helpers of the row kernels (quant_rows.hip, norm_block.hip): one
+// Device helpers of the row kernels (quant_rows.hip, norm_block.hip, mx4_rows.hip): one
 // workgroup holds one row of K values in registers. Device-only.
 //
 // Layout: the row is cut into blocks of 1024 values; wavefront w of W takes
@@ -138,6 +138,16 @@ __device__ __forceinline__ float row_reduce(float v, float* lds) {
   v = Op::of(v, lane_xor<2>(v));
   v = Op::of(v, lane_xor<4>(v));
   return Op::of(v, lane_xor<8>(v));
+}
+
+// 1 / sqrt(t), rounded once: the quotient of the root is off by a rounding of
+// either, and its residual 1 - t r^2, exact but for its own last rounding,
+// takes that out. (An infinite t has no residual: 0.)
+__device__ __forceinline__ float inv_root(float t) {
+  const float r = 1.0f / sqrtf(t);
+  const float h = t * r, lo = fmaf(t, r, -h);
+  const float e = fmaf(-lo, r, fmaf(-h, r, 1.0f));
+  return __float_as_uint(t) < 0x7F800000u ? fmaf(0.5f * r, e, r) : r;
 }
 
 // ------------------------------------------------------------ activations

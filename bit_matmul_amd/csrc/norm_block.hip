@@ -42,16 +42,6 @@ __device__ __forceinline__ float sum_squares(float (&v)[C][2][8], F f) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// 1 / sqrt(t), rounded once: the quotient of the root is off by a rounding of
-// either, and its residual 1 - t r^2, exact but for its own last rounding,
-// takes that out. (An infinite t has no residual: 0.)
-__device__ __forceinline__ float inv_root(float t) {
-  const float r = 1.0f / sqrtf(t);
-  const float h = t * r, lo = fmaf(t, r, -h);
-  const float e = fmaf(-lo, r, fmaf(-h, r, 1.0f));
-  return __float_as_uint(t) < 0x7F800000u ? fmaf(0.5f * r, e, r) : r;
-}
-
 // 1 / sqrt(mean(v^2) + eps). Where the sum of squares passes the largest
 // float, it is taken again of v 2^-80 (every thread of the workgroup sees the
 // same sum, so all take the branch together), with eps 2^-160 (0 below 2^11,

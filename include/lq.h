@@ -535,6 +535,161 @@ typedef struct lq_norm_block_args {
 lq_status lq_norm_block(const lq_norm_block_args* args, void* stream);
 
 /*
+ * Microscaled 4-bit layers: the layers of a model that are kept at 4 bits
+ * ([review] Limitations: the lifted code is weak near 4 bits and above),
+ * between the lifted ones and those at 8 bits. Weights and rows are 4-bit
+ * floating point with a power of two for every 32 values of a row (the MXFP4
+ * format of the OCP Microscaling Formats specification 1.0, which the matrix
+ * cores multiply as it is):
+ *
+ *     v = T (act(gate) .* x)                (act(gate) and T optional)
+ *     m = max |v_k| over a block of 32      (the last block of a row may be
+ *                                            shorter; blocks begin at k = 0)
+ *     e = floor(log2 m) - 2, at least -127  scale byte e + 127
+ *     q_k = v_k 2^-e rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ *           their negatives (codes 0..7, plus 8 for a negative), ties to the
+ *           even code, magnitudes above 6 to 6
+ *     y[n] = row_scale[n] * sum_blocks 2^(e_w + e_q) sum_k w[n][k] q[k]
+ *            (+ bias[n])
+ *
+ * A block of zeros has scale byte 0 and codes 0, a block that holds an
+ * infinity or a NaN has scale byte 255 (NaN) and codes 0, so the outputs of
+ * its row (or, of a weight, of its column) are NaN. Products are summed in
+ * fp32, in a fixed order.
+ *
+ * Codes: two in a byte, the even k in its low half; a row begins at a
+ * multiple of 16 bytes, owns 16 ceil(K / 32) bytes (the last row too), and rows
+ * are ld bytes apart, a multiple of 16. Rows at multiples of 128 bytes are read
+ * fastest.
+ *
+ * Scales: the byte of row n's block j lies at
+ *     ((n / 16) ceil(K / 256) + j / 8) 128 + 8 (n % 16) + 2 (j % 4) + j / 4 % 2
+ * (panels of 16 rows, 128 bytes for every 256 values of a panel; one load gives
+ * a matrix-core instruction's lanes what they need). The array has
+ * lq_mx4_scale_size bytes: whole panels, whole 256s; it is 16-byte aligned. Bytes of
+ * rows past the last and of blocks past K exist, and what they hold, and what
+ * codes past K hold, does not matter to the product. lq_mx4_quant_rows writes the bytes of
+ * its own rows and no others, those of blocks past K as 0.
+ *
+ * Weights are quantised by lq_mx4_quant_rows as well (their N rows of K, no
+ * gate, no T: of a layer with T they are W T^-1).
+ */
+#define LQ_MX4_MAX_K (1 << 20)   /* longest row */
+
+/* Bytes of the scales of `rows` rows of K. Errors: INVALID_ARG for a negative
+ * size, K < 1 or NULL bytes; UNSUPPORTED for K > LQ_MX4_MAX_K or rows > 2^28. */
+lq_status lq_mx4_scale_size(int64_t rows, int64_t K, size_t* bytes);
+
+/*
+ * 4-bit rows q and their scales of T (act(gate) .* x). Arguments as in
+ * lq_quant_rows; q: B rows, ldq bytes apart, whose 16 ceil(K / 32) bytes are
+ * written (codes past K as 0); scale: lq_mx4_scale_size(B, K) bytes. v is computed in fp32
+ * (T's sums times 1 / sqrt(hb); a block where one of them passes the largest
+ * float counts as one that holds an infinity); scale and codes are exactly
+ * those of that v. Errors: INVALID_ARG and UNSUPPORTED as lq_quant_rows, for
+ * K > LQ_MX4_MAX_K, and ldq below 16 ceil(K / 32).
+ */
+lq_status lq_mx4_quant_rows(const void* x, lq_dtype xtype, int64_t ldx, const void* gate, int64_t ldg,
+                            lq_act act, int64_t B, int64_t K, int32_t hb, const float* c, uint8_t* q,
+                            int64_t ldq, uint8_t* scale, void* stream);
+
+/* One 4-bit linear layer (all pointers device, caller-owned). */
+typedef struct lq_mx4_layer {
+  int64_t N;                 /* output features, at most 2^28, and B * N at most 2^36 */
+  int64_t K;                 /* input features */
+  int64_t ldw;               /* bytes from one row of w to the next, a multiple of 16 */
+  int32_t hb;                /* Hadamard block of T, as in lq_layer; 1: none */
+  int32_t reserved;          /* must be 0 */
+  const uint8_t* w;          /* N rows of K codes */
+  const uint8_t* w_scale;    /* their scales */
+  const float* c;            /* K channel scales of T; NULL: none (all one) */
+  const float* row_scale;    /* N scales; NULL: none (all one) */
+  const float* bias;         /* N values, or NULL */
+} lq_mx4_layer;
+
+/*
+ * The product of 4-bit rows (lq_mx4_quant_rows') with the layer's weights: y,
+ * B rows of N in ytype, ldy elements apart. The layer's hb and c are not used:
+ * T is a matter of the rows. y = sum * row_scale + bias in fp32, rounded once
+ * to ytype. Workspace and errors as lq_int8_gemm; UNSUPPORTED for K > LQ_MX4_MAX_K.
+ */
+lq_status lq_mx4_gemm_workspace_size(const lq_mx4_layer* layer, int64_t B, size_t* bytes);
+lq_status lq_mx4_gemm(const lq_mx4_layer* layer, const uint8_t* q, int64_t ldq,
+                      const uint8_t* scale, int64_t B, void* y, lq_dtype ytype, int64_t ldy,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * How lq_mx4_gemm would run, without running it (host only); fields as in
+ * lq_int8_plan_info. Errors: as lq_int8_gemm_plan.
+ */
+typedef struct lq_mx4_plan_info {
+  int32_t rows, tokens, ksplit, workgroups;
+} lq_mx4_plan_info;
+lq_status lq_mx4_gemm_plan(const lq_mx4_layer* layer, int64_t B, lq_mx4_plan_info* info);
+
+/*
+ * The whole 4-bit layer of act(gate) .* x: lq_mx4_quant_rows with the layer's
+ * T, then lq_mx4_gemm, the 4-bit rows in the workspace (behind its control
+ * area, which is left as it is). gate NULL: x alone. Errors: as those two.
+ */
+lq_status lq_mx4_linear_workspace_size(const lq_mx4_layer* layer, int64_t B, lq_dtype xtype,
+                                       size_t* bytes);
+lq_status lq_mx4_linear(const lq_mx4_layer* layer, const void* x, lq_dtype xtype, int64_t ldx,
+                        const void* gate, int64_t ldg, lq_act act, int64_t B, void* y,
+                        lq_dtype ytype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Norms of queries and keys for each head with the rotation by position, in
+ * one pass over the rows that a layer wrote. For token b, head h, x the head's
+ * dim values:
+ *
+ *     u = x / sqrt(mean(x^2) + eps) .* w     with LQ_QK_NORM, w = w_q or w_k
+ *                                            (else u = x)
+ *     t_i = pos[b] * freq[i]                 i < rot / 2, in fp64
+ *     (u_i, u_j) -> (u_i cos t_i - u_j sin t_i, u_j cos t_i + u_i sin t_i)
+ *         j = i + rot / 2; with LQ_QK_INTERLEAVED the pairs are (u_2i, u_2i+1)
+ *     u_k for k >= rot stay as they are
+ *
+ * in fp32, rounded once to dtype; angles are reduced in fp64, so that far
+ * positions keep their accuracy (the angle is off by 2^-51 of itself and 1e-7).
+ * NULL w: all ones. LQ_QK_ONE_PLUS: 1 + w in place of w. rot == 0: the norm alone. Element k of
+ * head h of token b lies at b ld + h ld_head + k: heads side by side in a row,
+ * or one after the other. q_out may be q and k_out k, with the same ld and ld_head;
+ * nothing else may overlap, nor may an output's heads. NULL q or k (with 0 heads):
+ * the other alone.
+ * Errors: INVALID_ARG for a NULL or misaligned pointer (pos, freq: their
+ * element's alignment), a negative size or ld, dim < 1, rot odd, negative or
+ * above dim, pos_bytes other than 4 or 8 (int32, int64), an output whose heads
+ * overlap, q_out == q (k_out == k) with other lds, LQ_QK_NORM with an eps that is not a positive normal float,
+ * unknown flags or dtype, reserved != 0; UNSUPPORTED for dim >
+ * LQ_QK_MAX_DIM, more than 2^16 heads, B > 2^20 or an ld above 2^40.
+ */
+#define LQ_QK_MAX_DIM 512
+#define LQ_QK_NORM 1u
+#define LQ_QK_ONE_PLUS 2u
+#define LQ_QK_INTERLEAVED 4u
+typedef struct lq_qk_norm_rope_args {
+  int64_t B;                 /* tokens */
+  const void* q;             /* dtype, as k and both outputs */
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t ldq, ldq_head, ldk, ldk_head;
+  int64_t ldq_out, ldq_out_head, ldk_out, ldk_out_head;
+  const float* w_q;          /* dim values, or NULL */
+  const float* w_k;
+  const void* pos;           /* B positions of pos_bytes each (unused with rot 0) */
+  const double* freq;        /* rot / 2 angles a position */
+  int32_t q_heads, k_heads, dim, rot;
+  int32_t dtype;             /* lq_dtype */
+  int32_t pos_bytes;
+  float eps;
+  uint32_t flags;            /* LQ_QK_* */
+  uint64_t reserved;         /* must be 0 */
+} lq_qk_norm_rope_args;
+lq_status lq_qk_norm_rope(const lq_qk_norm_rope_args* args, void* stream);
+
+/*
  * Prepare a workspace for first use: zero-fill its control area (the first
  * min(ws_bytes, LQ_WS_CONTROL_BYTES) bytes, with a kernel on `stream`).
  * Errors: INVALID_ARG for a NULL or unaligned ws with ws_bytes > 0.
