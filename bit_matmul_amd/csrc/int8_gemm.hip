@@ -50,16 +50,6 @@ __device__ __forceinline__ i32x4 acc_take(const i32x4& acc) {
   return (i32x4){v[0], v[1], v[2], v[3]};
 }
 
-// Tile t of the order in which an XCD takes them.
-struct TilePlace {
-  int n, b;
-};
-__device__ __forceinline__ TilePlace tile_place(int t, int tiles_n, int tiles_b, int group_n) {
-  const int grp = t / (group_n * tiles_b), in = t % (group_n * tiles_b);
-  const int gn = min(group_n, tiles_n - grp * group_n);
-  return {grp * group_n + in % gn, in / gn};
-}
-
 // acc += a c, in place. (The builtin leaves the choice of the result's
 // registers to the compiler: with two steps in a row it took others, and
 // moved and spilled 256 sums.) The compiler awaits an asm's operands as before

@@ -1,5 +1,5 @@
 // Device helpers of the 8-bit products (int8_gemm.hip, int8_few.hip,
-// int8_token.hip).
+// int8_token.hip), some of them shared by the 4-bit ones.
 #pragma once
 
 #include "lq_8bit.h"
@@ -17,6 +17,16 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_s_waitcnt(3 << 14 | 7 << 4 | 15);
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Tile t of the order in which an XCD takes them.
+struct TilePlace {
+  int n, b;
+};
+__device__ __forceinline__ TilePlace tile_place(int t, int tiles_n, int tiles_b, int group_n) {
+  const int grp = t / (group_n * tiles_b), in = t % (group_n * tiles_b);
+  const int gn = min(group_n, tiles_n - grp * group_n);
+  return {grp * group_n + in % gn, in / gn};
 }
 
 // Outputs n .. n + 3 (those below N) of token b from their sums, with the
