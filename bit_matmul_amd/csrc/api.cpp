@@ -1390,10 +1390,14 @@ lq_status lq_mx4_linear(const lq_mx4_layer* layer, const void* x, lq_dtype xtype
   char* base = static_cast<char*>(ws);
   uint8_t* q = reinterpret_cast<uint8_t*>(base + w.off_q);
   uint8_t* scale = reinterpret_cast<uint8_t*>(base + w.off_scale);
-  s = hip_status(lq::launch_mx4_rows(mx4_row_args(x, xtype, ldx, gate, ldg, act, B, layer->K, layer->hb,
-                                                  layer->c, q, w.ldq, scale), (hipStream_t)stream));
+  const lq::Mx4Rows p =
+      mx4_row_args(x, xtype, ldx, gate, ldg, act, B, layer->K, layer->hb, layer->c, q, w.ldq, scale);
+  const lq::Mx4Gemm gemm = mx4_args(layer, q, w.ldq, scale, B, y, ytype, ldy);
+  if (const int rows = lq::mx4_token_rows(p, layer->N, w.plan); rows > 0)
+    return hip_status(lq::launch_mx4_token(p, gemm, rows, (hipStream_t)stream));
+  s = hip_status(lq::launch_mx4_rows(p, (hipStream_t)stream));
   if (s != LQ_OK) return s;
-  return hip_status(lq::launch_mx4_gemm(mx4_args(layer, q, w.ldq, scale, B, y, ytype, ldy), w.plan,
+  return hip_status(lq::launch_mx4_gemm(gemm, w.plan,
                                         mx4_partial(w.plan, ws, w.off_partial), (hipStream_t)stream));
 }
 

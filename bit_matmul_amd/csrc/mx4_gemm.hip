@@ -420,6 +420,8 @@ constexpr TileCost kTiles[] = {
     {128, 128, 128, 1, 0.469f, 0.058f, 2.6f, false}, {128, 64, 256, 1, 0.829f, 0.013f, 2.2f, false},
     {64, 128, 256, 1, 0.530f, 0.323f, 2.1f, false},  {64, 64, 256, 2, 0.728f, 0.225f, 1.5f, false},
     {64, 32, 256, 3, 0.424f, 0.190f, 1.74f, false},  {32, 32, 256, 2, 0.140f, 0.202f, 1.36f, false},
+    {16, 4, 1024, 4, 0.369f, 0.511f, 0.72f, true},   {16, 8, 1024, 3, 0.072f, 0.672f, 0.81f, true},
+    {16, 16, 1024, 2, 0.112f, 0.593f, 1.12f, true},  {32, 16, 1024, 1, 0.007f, 1.171f, 1.45f, true},
 };
 constexpr float kJoinUs = 5.0f, kJoinBytesPerUs = 7.0e6f;
 constexpr float kStreamBytesPerUs[2] = {4.72e6f, 6.3e6f}, kHidden[2] = {0.216f, 0.298f};     // tiles, few
@@ -434,6 +436,7 @@ Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus) {
   float best_us = 0.0f;
   const int64_t bytes = mx4_row_bytes(K);
   for (const TileCost& c : kTiles) {
+    if (c.few && (B > c.tokens || (c.tokens > 4 && B <= c.tokens / 2))) continue;   // (no more codes than needed)
     const int64_t tiles = ((N + c.rows - 1) / c.rows) * ((B + c.tokens - 1) / c.tokens);
     const float stream = (float)N * (float)bytes / kStreamBytesPerUs[c.few];      // the weights'
     const int64_t slots = (int64_t)cus * c.per_cu, steps = (bytes + c.bytes - 1) / c.bytes;
@@ -451,7 +454,7 @@ Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus) {
       const size_t partial = ks > 1 ? (size_t)units * c.rows * c.tokens * 4 : 0;
       if (ks > 1) us += kJoinUs + 2.0f * (float)partial / kJoinBytesPerUs;
       if (best.rows == 0 || us < best_us) {
-        best = {c.rows, c.tokens, ks, (int)tiles, partial};
+        best = {c.rows, c.tokens, ks, (int)tiles, c.few, partial};
         best_us = us;
       }
     }
@@ -461,6 +464,7 @@ Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus) {
 
 hipError_t launch_mx4_gemm(const Mx4Gemm& p, const Mx4Plan& plan, float* partial, hipStream_t stream) {
   (void)hipGetLastError();   // clear a stale error of an earlier runtime call
+  if (plan.few) return launch_mx4_few(p, plan, stream);
   switch (plan.rows / 32 * 16 + plan.tokens / 32) {
     case 0x88: enqueue_tile<8, 8, 2, 128>(p, plan, partial, stream); break;
     case 0x78: enqueue_tile<7, 8, 2, 128>(p, plan, partial, stream); break;
