@@ -394,6 +394,9 @@ def _here(t, name: str):
     """(address, bytes) of a workspace, or of none."""
     if t is None:
         return None, 0
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.is_cuda and t.is_contiguous() and
+            t.get_device() == _current_device()):
+        return t.data_ptr(), t.numel()
     ptr = _dev(t, name)
     if t.get_device() != _current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
@@ -606,7 +609,8 @@ def lq_mx4_gemm(layer: LQMx4Layer, q, scale, B, y, ws=None, stream=None) -> None
     qp, ldq = _rows4(q, "q", B, layer.K)
     yp, ldy = _rows(y, "y", B, layer.N)
     wsp, ws_bytes = _here(ws, "ws")
-    _layer_here(layer)
+    if layer.device != _current_device():
+        _layer_here(layer)
     _check(_lib.LIB.lq_mx4_gemm(ctypes.byref(layer), qp, ldq, _scales4(scale, "scale", B, layer.K), B, yp,
                                 _dtype(y, "y"), ldy, wsp, ws_bytes, _stream(stream)), "lq_mx4_gemm")
 
@@ -629,82 +633,94 @@ def lq_mx4_linear_workspace_size(layer: LQMx4Layer, B, xtype) -> int:
 def lq_mx4_linear(layer: LQMx4Layer, x, B, y, ws=None, gate=None, act=LQ_ACT_NONE, stream=None) -> None:
     """The whole 4-bit layer of act(gate) * x: 4-bit rows, then the product."""
     xp, ldx = _rows(x, "x", B, layer.K)
-    gp, ldg = _gate(gate, x, B, layer.K)
+    gp, ldg = (None, 0) if gate is None else _gate(gate, x, B, layer.K)
     yp, ldy = _rows(y, "y", B, layer.N)
     wsp, ws_bytes = _here(ws, "ws")
-    _layer_here(layer)
+    if layer.device != _current_device():
+        _layer_here(layer)
     _check(_lib.LIB.lq_mx4_linear(ctypes.byref(layer), xp, _dtype(x, "x"), ldx, gp, ldg, act, B, yp,
                                   _dtype(y, "y"), ldy, wsp, ws_bytes, _stream(stream)),
            "lq_mx4_linear")
 
 
-def _head_rows(t, name: str, B: int, heads: int, dim: int):
+def _head_rows(t, name: str, shape, dtype):
     """(address, token stride, head stride) of a GPU tensor (tokens, heads, dim)
     whose heads are dense."""
+    # (one test for a call that is right, as _rows)
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and
+            t.get_device() == _current_device()):
+        ld, ld_head, step = t.stride()
+        if step == 1 or shape[2] == 1:
+            return t.data_ptr(), ld, ld_head
+        raise ValueError(f"{name}'s heads must be dense")
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{name} must be a GPU tensor of three dimensions")
-    if t.shape[0] < B or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, ({B}, {heads}, {dim}) is needed")
-    if t.get_device() != _current_device():
-        raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    ld, ld_head, step = t.stride()
-    if step != 1 and dim > 1:
-        raise ValueError(f"{name}'s heads must be dense")
-    return t.data_ptr(), ld, ld_head
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, as the others")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} is needed")
+    raise ValueError(f"{name} is on {t.device}, which is not the current device")
+
+
+def _qk_part(x, out, name: str, tokens, dim, dtype):
+    """Addresses, strides and number of the heads of one of the two parts."""
+    if out is None:
+        raise ValueError(f"{name}_out is needed with {name}")
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim:
+        raise ValueError(f"q and k must be (tokens, heads, dim) with the same tokens and dim, {name} is {tuple(shape)}")
+    xp, ld, ld_head = _head_rows(x, name, shape, dtype)
+    op, ldo, ldo_head = (xp, ld, ld_head) if out is x else _head_rows(out, name + "_out", shape, dtype)
+    return xp, op, ld, ld_head, ldo, ldo_head, shape[1]
 
 
 _QK_ARGS = struct.Struct("q4Q8q4Q6ifIQ")
 assert _QK_ARGS.size == ctypes.sizeof(LQQkNormRopeArgs)
 _QK_NORM_ROPE = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, ctypes.c_void_p)(("lq_qk_norm_rope", _lib.LIB))
 _POS_BYTES = {torch.int32: 4, torch.int64: 8}
+_NO_HEADS = (0,) * 7
+
+
+def _flat(t, name: str) -> int:
+    """The address of a dense tensor on the current device."""
+    if t.is_cuda and t.is_contiguous() and t.get_device() == _current_device():
+        return t.data_ptr()
+    _dev(t, name)
+    raise ValueError(f"{name} is on {t.device}, which is not the current device")
 
 
 def lq_qk_norm_rope(pos, freq, q=None, k=None, q_out=None, k_out=None, norm=True, w_q=None, w_k=None,
                     one_plus=False, eps=1e-5, interleaved=False, stream=None) -> None:
     """Norms of queries and keys for each head and the rotation by position
     (lq.h gives the formulas). q, k and their outputs: (tokens, heads, dim) of
-    one dtype, any token and head strides; an output may be its input. pos: int32 or int64, one for
-    each token; freq: float64, an angle a position for each pair of values (2 of
-    them for each: the first 2 * freq.numel() of a head are rotated)."""
-    some = q if q is not None else k
+    one dtype, any token and head strides; an output may be its input. pos: int32
+    or int64, one for each token; freq: float64, an angle a position for each
+    pair of values (the first 2 * freq.numel() values of a head are rotated);
+    None: the norm alone."""
+    some = k if q is None else q
     if some is None:
         raise ValueError("q or k is needed")
-    dt = _dtype(some, "q" if q is not None else "k")
     if some.dim() != 3:
         raise ValueError("q and k must be GPU tensors of three dimensions")
     B, _, dim = some.shape
-    ptrs, lds, heads = [], [], []
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            if out is not None:
-                raise ValueError(f"{name}_out without {name}")
-            ptrs += [0, 0]
-            lds += [0, 0, 0, 0]
-            heads.append(0)
-            continue
-        if out is None or x.dtype != some.dtype or out.dtype != some.dtype:
-            raise ValueError(f"{name} and {name}_out must be given, of one dtype")
-        n = x.shape[1] if x.dim() == 3 else 0
-        if x.dim() == 3 and x.shape[0] != B:
-            raise ValueError("q and k must have the same tokens")
-        xp, ld, ldh = _head_rows(x, name, B, n, dim)
-        op, ldo, ldoh = _head_rows(out, name + "_out", B, n, dim)
-        ptrs += [xp, op]
-        lds += [ld, ldh, ldo, ldoh]
-        heads.append(n)
-    rot = 0 if freq is None else 2 * freq.numel()
-    pp = fp = 0
+    dtype = some.dtype
+    dt = _dtype(some, "k" if q is None else "q")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output without its input")
+    qp, qop, ldq, ldqh, ldqo, ldqoh, q_heads = _NO_HEADS if q is None else _qk_part(q, q_out, "q", B, dim, dtype)
+    kp, kop, ldk, ldkh, ldko, ldkoh, k_heads = _NO_HEADS if k is None else _qk_part(k, k_out, "k", B, dim, dtype)
+    rot = pp = fp = 0
     width = 8
-    if rot:
+    if freq is not None and freq.numel():
+        rot = 2 * freq.numel()
         width = _POS_BYTES.get(pos.dtype)
-        if width is None or freq.dtype != torch.float64:
+        if width is None or freq.dtype is not torch.float64:
             raise ValueError("pos must be int32 or int64 and freq float64")
         if pos.numel() < B:
             raise ValueError(f"pos must hold {B} positions")
-        pp, fp = _here(pos, "pos")[0], _here(freq, "freq")[0]
+        pp, fp = _flat(pos, "pos"), _flat(freq, "freq")
     flags = ((LQ_QK_NORM if norm else 0) | (LQ_QK_ONE_PLUS if one_plus else 0) |
              (LQ_QK_INTERLEAVED if interleaved else 0))
-    p = _QK_ARGS.pack(B, ptrs[0], ptrs[2], ptrs[1], ptrs[3], lds[0], lds[1], lds[4], lds[5], lds[2], lds[3], lds[6],
-                      lds[7], _vec(w_q, "w_q", dim) or 0, _vec(w_k, "w_k", dim) or 0, pp, fp, *heads, dim, rot, dt,
-                      width, eps, flags, 0)
+    p = _QK_ARGS.pack(B, qp, kp, qop, kop, ldq, ldqh, ldk, ldkh, ldqo, ldqoh, ldko, ldkoh, _vec(w_q, "w_q", dim) or 0,
+                      _vec(w_k, "w_k", dim) or 0, pp, fp, q_heads, k_heads, dim, rot, dt, width, eps, flags, 0)
     _check(_QK_NORM_ROPE(p, _stream(stream)), "lq_qk_norm_rope")

@@ -95,6 +95,7 @@ class LQNormBlockArgs(ctypes.Structure):
 
 class LQMx4Layer(ctypes.Structure):
     """Mirror of ``struct lq_mx4_layer``."""
+    device = None           # of its tensors, where it is known
     _fields_ = [
         ("N", c_int64), ("K", c_int64), ("ldw", c_int64), ("hb", c_int32), ("reserved", c_int32),
         ("w", c_void_p), ("w_scale", c_void_p), ("c", c_void_p), ("row_scale", c_void_p),

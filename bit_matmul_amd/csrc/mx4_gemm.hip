@@ -430,31 +430,34 @@ constexpr int64_t kMaxTiles = 1 << 22;    // (a launch has fewer than 2^32 threa
 
 }  // namespace
 
+// (A call makes its plan: 32-bit arithmetic, and of a tile no more splits than
+// could fill the device. At most 2^26 workgroups and 2^13 steps.)
 Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus) {
   if (cus <= 0) cus = 256;
   Mx4Plan best{};
   float best_us = 0.0f;
-  const int64_t bytes = mx4_row_bytes(K);
+  const uint32_t bytes = (uint32_t)mx4_row_bytes(K), ucus = (uint32_t)cus;
   for (const TileCost& c : kTiles) {
     if (c.few && (B > c.tokens || (c.tokens > 4 && B <= c.tokens / 2))) continue;   // (no more codes than needed)
-    const int64_t tiles = ((N + c.rows - 1) / c.rows) * ((B + c.tokens - 1) / c.tokens);
+    const uint32_t tiles_n = ((uint32_t)N + c.rows - 1) / c.rows, tiles_b = ((uint32_t)B + c.tokens - 1) / c.tokens;
+    if ((uint64_t)tiles_n * tiles_b > (uint64_t)kMaxTiles && &c != kTiles) continue;
+    const uint32_t tiles = tiles_n * tiles_b, slots = ucus * c.per_cu, steps = (bytes + c.bytes - 1) / c.bytes;
     const float stream = (float)N * (float)bytes / kStreamBytesPerUs[c.few];      // the weights'
-    const int64_t slots = (int64_t)cus * c.per_cu, steps = (bytes + c.bytes - 1) / c.bytes;
-    if (tiles > kMaxTiles && &c != kTiles) continue;
-    for (int ks = 1; ks <= kMaxSplit && ks <= steps; ++ks) {
-      if (ks > 1 && (c.few || tiles * ks > 4 * (int64_t)cus)) break;
+    uint32_t most = c.few ? 1u : 4u * ucus / tiles;
+    most = most < 1u ? 1u : most > (uint32_t)kMaxSplit ? (uint32_t)kMaxSplit : most;
+    for (uint32_t ks = 1; ks <= most && ks <= steps; ++ks) {
       const float len = (float)((steps + ks - 1) / ks);
-      const int64_t units = tiles * ks, full = units / slots, rem = units % slots;
+      const uint32_t units = tiles * ks, full = units / slots, rem = units - full * slots;
       float us = (float)full * (len * (c.step + c.share * c.per_cu) + c.ends);
       if (rem > 0) {
-        const float load = 0.5f * ((float)rem / cus + (float)((rem + cus - 1) / cus));
+        const float load = 0.5f * ((float)rem / (float)ucus + (float)((rem + ucus - 1) / ucus));
         us += len * (c.step + c.share * load) + c.ends;
       }
       us = us > stream ? us + kHidden[c.few] * stream : stream + kHidden[c.few] * us;
       const size_t partial = ks > 1 ? (size_t)units * c.rows * c.tokens * 4 : 0;
       if (ks > 1) us += kJoinUs + 2.0f * (float)partial / kJoinBytesPerUs;
       if (best.rows == 0 || us < best_us) {
-        best = {c.rows, c.tokens, ks, (int)tiles, c.few, partial};
+        best = {c.rows, c.tokens, (int)ks, (int)tiles, c.few, partial};
         best_us = us;
       }
     }
