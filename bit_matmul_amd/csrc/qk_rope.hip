@@ -1,12 +1,14 @@
 // Norms of queries and keys for each head with the rotation by position
-// (include/lq.h gives the formulas), one token to a workgroup.
+// (include/lq.h gives the formulas).
 //
 // A lane holds 16 values of a head, 8 rotated pairs: of two halves 8 values
 // each, of neighbours 16 in a row, so that no pair lies in two lanes; the
 // values behind the rotated ones follow, 16 to a lane. 1 to 64 lanes make a
-// head, whose sum of squares is a few lane exchanges. The token's angles are
-// computed once by the workgroup, in fp64 up to their fraction of a turn, and
-// read from LDS.
+// head, whose sum of squares is a few lane exchanges, and a wavefront a group of
+// heads. Wavefronts do not meet: each takes a part of one token's groups,
+// computes the token's angles for itself (one to a lane, in fp64 up to the
+// fraction of a turn) and passes them round through LDS of its own, while its
+// first groups are on their way.
 #include "lq_qk.h"
 
 #include "lq_rows.h"
@@ -16,21 +18,19 @@ namespace {
 
 // 8 values at p (at its element's alignment), those from n on as zero.
 template <bool kBF16, bool kWhole>
-__device__ __forceinline__ void load8(const void* p, int n, float (&v)[8]) {
-  RowPiece<kBF16> w;
+__device__ __forceinline__ void load8(const void* p, int n, RowPiece<kBF16>& to) {
 #pragma unroll
-  for (int i = 0; i < (kBF16 ? 4 : 8); ++i) w.w[i] = 0;
+  for (int i = 0; i < (kBF16 ? 4 : 8); ++i) to.w[i] = 0;
   if (n >= 8) {
-    __builtin_memcpy(w.w, p, sizeof(w.w));
+    __builtin_memcpy(to.w, p, sizeof(to.w));
   } else if constexpr (!kWhole) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < n) {
-        if constexpr (kBF16) w.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-        else w.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        if constexpr (kBF16) to.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+        else to.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
       }
   }
-  w.get(v);
 }
 template <bool kBF16, bool kWhole>
 __device__ __forceinline__ void store8(void* p, int n, const float (&v)[8]) {
@@ -67,59 +67,103 @@ __device__ __forceinline__ float head_sum(float v, int lanes_log) {
   return v;
 }
 
+// The pieces of a lane: 8 values from off[0] on and 8 from off[1] on, of which
+// n[0] and n[1] exist.
+struct Place {
+  int off[2], n[2];
+};
+
+constexpr int kBatch = 2;        // groups on their way together, and as many behind them
+
 template <bool kBF16, bool kInterleaved, bool kWhole>
-__global__ __launch_bounds__(1024) void qk_norm_rope_kernel(QkNormRope p, int lanes_log) {
-  __shared__ float turn[2][kQkMaxDim / 2];
-  const int64_t b = blockIdx.x;
-  const int half = p.rot / 2;
-  for (int i = threadIdx.x; i < kQkMaxDim / 2; i += (int)blockDim.x) {
-    float s = 0.0f, c = 1.0f;
-    if (i < half) {
-      const double at = p.pos64 ? (double)reinterpret_cast<const int64_t*>(p.pos)[b]
-                                : (double)reinterpret_cast<const int32_t*>(p.pos)[b];
-      double t = at * p.freq[i] * 0.15915494309189533577;      // turns
-      t -= rint(t);
-      sincospif(2.0f * (float)t, &s, &c);
-    }
-    turn[0][i] = c;
-    turn[1][i] = s;
-  }
-  __syncthreads();
+__global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lanes_log, int parts) {
+  __shared__ float turns[4][2][kQkMaxDim / 2];
+  const int64_t unit = (int64_t)blockIdx.x * 4 + wave_id();
+  const int64_t b = unit / parts;
+  if (b >= p.B) return;
+  const int part = (int)(unit - b * parts);
+  float (&turn)[2][kQkMaxDim / 2] = turns[wave_id()];
   constexpr int kSize = kBF16 ? 2 : 4;
-  const int lane = threadIdx.x & 63;
-  const int per = 64 >> lanes_log;                       // heads of a wavefront
+  const int lane = threadIdx.x & 63, half = p.rot / 2;
+  const int per = 64 >> lanes_log;                       // heads of a group
   const int j = lane & ((1 << lanes_log) - 1), h_in = lane >> lanes_log;
   const int rl = (p.rot + 15) / 16;                      // lanes that rotate
   const bool rotates = j < rl;
-  int off[2], n[2];
+  Place at;
   if (rotates && !kInterleaved) {
-    off[0] = 8 * j;
-    off[1] = half + 8 * j;
-    n[0] = n[1] = min(8, half - 8 * j);
+    at.off[0] = 8 * j;
+    at.off[1] = half + 8 * j;
+    at.n[0] = at.n[1] = min(8, half - 8 * j);
   } else {
     const int end = rotates ? p.rot : p.dim;
-    off[0] = rotates ? 16 * j : p.rot + 16 * (j - rl);
-    off[1] = off[0] + 8;
-    n[0] = max(0, min(8, end - off[0]));
-    n[1] = max(0, min(8, end - off[1]));
+    at.off[0] = rotates ? 16 * j : p.rot + 16 * (j - rl);
+    at.off[1] = at.off[0] + 8;
+    at.n[0] = max(0, min(8, end - at.off[0]));
+    at.n[1] = max(0, min(8, end - at.off[1]));
+  }
+  const int qu = (p.part[0].heads + per - 1) / per, groups = qu + (p.part[1].heads + per - 1) / per;
+  const int g0 = groups * part / parts, g1 = groups * (part + 1) / parts;
+
+  RowPiece<kBF16> in[2][kBatch][2];
+  auto head = [&](int g) __attribute__((always_inline)) { return (g < qu ? g : g - qu) * per + h_in; };
+  auto load = [&](RowPiece<kBF16> (&to)[kBatch][2], int g) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      // (past the last group: that one again; heads past the last: the first)
+      const int gi = min(g + i, g1 - 1);
+      const QkHeads& t = p.part[gi < qu ? 0 : 1];
+      const int h = head(gi) < t.heads ? head(gi) : 0;
+      const char* const x = reinterpret_cast<const char*>(t.x) + (b * t.ld + h * t.ld_head) * kSize;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) load8<kBF16, kWhole>(x + at.off[k] * kSize, at.n[k], to[i][k]);
+    }
+  };
+  load(in[0], g0);
+
+  if (half > 0) {
+    const double pos = p.pos64 ? (double)reinterpret_cast<const int64_t*>(p.pos)[b]
+                               : (double)reinterpret_cast<const int32_t*>(p.pos)[b];
+    for (int i = lane; i < half; i += 64) {
+      double t = pos * p.freq[i] * 0.15915494309189533577;      // turns
+      t -= rint(t);
+      sincospif(2.0f * (float)t, &turn[1][i], &turn[0][i]);
+    }
+    // (the wavefront's own stores, before its reads)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_s_waitcnt(3 << 14 | 7 << 4 | 15);
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
   float c[8], s[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    c[k] = rotates ? turn[0][min(8 * j + k, kQkMaxDim / 2 - 1)] : 1.0f;
-    s[k] = rotates ? turn[1][min(8 * j + k, kQkMaxDim / 2 - 1)] : 0.0f;
+    // (places past the last angle: an angle of this token, whose product is dropped)
+    c[k] = rotates ? turn[0][min(8 * j + k, half - 1)] : 1.0f;
+    s[k] = rotates ? turn[1][min(8 * j + k, half - 1)] : 0.0f;
   }
-  const int qu = (p.part[0].heads + per - 1) / per, units = qu + (p.part[1].heads + per - 1) / per;
-  for (int u = wave_id(); u < units; u += (int)blockDim.x >> 6) {
-    const QkHeads& t = p.part[u < qu ? 0 : 1];
-    const int h = (u < qu ? u : u - qu) * per + h_in;
-    const bool mine = h < t.heads;
-    const char* const x = reinterpret_cast<const char*>(t.x) + (b * t.ld + (mine ? h : 0) * t.ld_head) * kSize;
-    char* const o = reinterpret_cast<char*>(t.out) + (b * t.ldo + (mine ? h : 0) * t.ldo_head) * kSize;
+  float w[2][8];
+  auto weights = [&](const QkHeads& t) __attribute__((always_inline)) {
+    const float plus = p.one_plus ? 1.0f : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (t.w != nullptr) {
+        RowPiece<false> piece;
+        load8<false, kWhole>(t.w + at.off[i], at.n[i], piece);
+        piece.get(w[i]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[i][k] = t.w != nullptr ? plus + w[i][k] : 1.0f;
+    }
+  };
+  if (p.norm) weights(p.part[g0 < qu ? 0 : 1]);
+
+  auto one = [&](const RowPiece<kBF16> (&piece)[2], int g) __attribute__((always_inline)) {
+    if (g >= g1) return;
+    const QkHeads& t = p.part[g < qu ? 0 : 1];
     float v[2][8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) load8<kBF16, kWhole>(x + off[i] * kSize, n[i], v[i]);
+    for (int i = 0; i < 2; ++i) piece[i].get(v[i]);
     if (p.norm) {
+      if (g == qu && g != g0) weights(t);
       float q[2] = {};
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -134,8 +178,8 @@ __global__ __launch_bounds__(1024) void qk_norm_rope_kernel(QkNormRope p, int la
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float w = v[i][k] * 0x1p-80f;
-            z = fmaf(w, w, z);
+            const float u = v[i][k] * 0x1p-80f;
+            z = fmaf(u, u, z);
           }
         z = head_sum(z, lanes_log);
         if (!(sum <= 3.0e38f)) {
@@ -146,14 +190,10 @@ __global__ __launch_bounds__(1024) void qk_norm_rope_kernel(QkNormRope p, int la
             for (int k = 0; k < 8; ++k) v[i][k] *= 0x1p-40f;
         }
       }
-      const float plus = p.one_plus ? 1.0f : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float w[8];
-        if (t.w != nullptr) load8<false, kWhole>(t.w + off[i], n[i], w);
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = v[i][k] * r * (t.w != nullptr ? plus + w[k] : 1.0f);
-      }
+        for (int k = 0; k < 8; ++k) v[i][k] = v[i][k] * r * w[i][k];
     }
     if (rotates) {
 #pragma unroll
@@ -165,23 +205,37 @@ __global__ __launch_bounds__(1024) void qk_norm_rope_kernel(QkNormRope p, int la
         d = fmaf(d0, c[k], a0 * s[k]);
       }
     }
-    if (mine) {
+    const int h = head(g);
+    if (h < t.heads) {
+      char* const o = reinterpret_cast<char*>(t.out) + (b * t.ldo + h * t.ldo_head) * kSize;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) store8<kBF16, kWhole>(o + off[i] * kSize, n[i], v[i]);
+      for (int i = 0; i < 2; ++i) store8<kBF16, kWhole>(o + at.off[i] * kSize, at.n[i], v[i]);
     }
+  };
+  for (int g = g0; g < g1; g += 2 * kBatch) {
+    if (g + kBatch < g1) load(in[1], g + kBatch);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) one(in[0][i], g + i);
+    if (g + 2 * kBatch < g1) load(in[0], g + 2 * kBatch);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) one(in[1][i], g + kBatch + i);
   }
 }
 
 template <bool kBF16>
-void enqueue(const QkNormRope& p, bool whole, int lanes_log, dim3 grid, dim3 block, hipStream_t stream) {
+void enqueue(const QkNormRope& p, bool whole, int lanes_log, int parts, dim3 grid, hipStream_t stream) {
+  const dim3 block(256);
   if (p.interleaved) {
-    if (whole) hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, true, true>), grid, block, 0, stream, p, lanes_log);
-    else hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, true, false>), grid, block, 0, stream, p, lanes_log);
+    if (whole) hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, true, true>), grid, block, 0, stream, p, lanes_log, parts);
+    else hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, true, false>), grid, block, 0, stream, p, lanes_log, parts);
   } else {
-    if (whole) hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, false, true>), grid, block, 0, stream, p, lanes_log);
-    else hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, false, false>), grid, block, 0, stream, p, lanes_log);
+    if (whole) hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, false, true>), grid, block, 0, stream, p, lanes_log, parts);
+    else hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, false, false>), grid, block, 0, stream, p, lanes_log, parts);
   }
 }
+
+// Wavefronts that keep the device busy.
+constexpr int64_t kWaves = 4096;
 
 }  // namespace
 
@@ -191,11 +245,13 @@ hipError_t launch_qk_norm_rope(const QkNormRope& p, hipStream_t stream) {
   int lanes_log = 0;
   while ((1 << lanes_log) < lanes) ++lanes_log;
   const int per = 64 >> lanes_log;
-  const int units = (p.part[0].heads + per - 1) / per + (p.part[1].heads + per - 1) / per;
+  const int groups = (p.part[0].heads + per - 1) / per + (p.part[1].heads + per - 1) / per;
+  const int64_t want = (kWaves + p.B - 1) / p.B;
+  const int parts = want < groups ? (int)want : groups;
   const bool whole = p.rot % 16 == 0 && p.dim % 16 == 0;
-  const dim3 grid((unsigned)p.B), block(64u * (unsigned)(units < 16 ? units : 16));
-  if (p.bf16) enqueue<true>(p, whole, lanes_log, grid, block, stream);
-  else enqueue<false>(p, whole, lanes_log, grid, block, stream);
+  const dim3 grid((unsigned)((p.B * parts + 3) / 4));
+  if (p.bf16) enqueue<true>(p, whole, lanes_log, parts, grid, stream);
+  else enqueue<false>(p, whole, lanes_log, parts, grid, stream);
   return hipGetLastError();
 }
 
