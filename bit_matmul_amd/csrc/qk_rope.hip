@@ -16,42 +16,94 @@
 namespace lq {
 namespace {
 
-// 8 values at p (at its element's alignment), those from n on as zero.
+// A lane's piece of a head: n values (at most 8) from `off` on.
+struct Place {
+  int off, n;
+};
+__device__ __forceinline__ Place place(int off, int end) { return {off, max(0, min(8, end - off))}; }
+
+// Loaded at its element's alignment, those that do not exist as zero: 8 at
+// once, or 4, 2 and 1 of them. kWhole: 8 or none.
+typedef uint32_t __attribute__((ext_vector_type(4), aligned(2))) u32x4_u;
+typedef uint32_t __attribute__((ext_vector_type(2), aligned(2))) u32x2_u;
+typedef uint32_t __attribute__((aligned(2))) u32_u;
 template <bool kBF16, bool kWhole>
-__device__ __forceinline__ void load8(const void* p, int n, RowPiece<kBF16>& to) {
+__device__ __forceinline__ void load8(RowPiece<kBF16>& to, const void* head, const Place& at) {
+  const char* const p = reinterpret_cast<const char*>(head) + at.off * (kBF16 ? 2 : 4);
+  const bool four = at.n & 4, pair = at.n & 2, odd = at.n & 1;
+  if constexpr (kBF16) {
+    u32x4_u all = {0, 0, 0, 0};
+    if (at.n >= 8) all = *reinterpret_cast<const u32x4_u*>(p);
+    if (!kWhole && at.n < 8) {
+      u32x2_u quad = {0, 0};
+      uint32_t two = 0, one = 0;
+      if (four) quad = *reinterpret_cast<const u32x2_u*>(p);
+      if (pair) two = *reinterpret_cast<const u32_u*>(p + 2 * (at.n & 4));
+      if (odd) one = *reinterpret_cast<const uint16_t*>(p + 2 * (at.n & 6));
+      const uint32_t first = pair ? two : one, second = pair ? one : 0u;
+      all = four ? (u32x4_u){quad[0], quad[1], first, second} : (u32x4_u){first, second, 0, 0};
+    }
 #pragma unroll
-  for (int i = 0; i < (kBF16 ? 4 : 8); ++i) to.w[i] = 0;
-  if (n >= 8) {
-    __builtin_memcpy(to.w, p, sizeof(to.w));
-  } else if constexpr (!kWhole) {
+    for (int i = 0; i < 4; ++i) to.w[i] = all[i];
+  } else {
+    u32x4_u low = {0, 0, 0, 0}, high = {0, 0, 0, 0};
+    if (at.n >= 4) low = *reinterpret_cast<const u32x4_u*>(p);
+    if (at.n >= 8) high = *reinterpret_cast<const u32x4_u*>(p + 16);
+    if (!kWhole && at.n < 8) {
+      u32x2_u two = {0, 0};
+      uint32_t one = 0;
+      if (pair) two = *reinterpret_cast<const u32x2_u*>(p + 4 * (at.n & 4));
+      if (odd) one = *reinterpret_cast<const uint32_t*>(p + 4 * (at.n & 6));
+      const u32x4_u rest = {pair ? two[0] : one, two[1], pair ? one : 0u, 0};
+      if (four) high = rest;
+      else low = rest;
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) {
-        if constexpr (kBF16) to.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-        else to.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-      }
+    for (int i = 0; i < 4; ++i) to.w[i] = low[i], to.w[4 + i] = high[i];
   }
 }
 template <bool kBF16, bool kWhole>
-__device__ __forceinline__ void store8(void* p, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void* head, const Place& at, const float (&v)[8]) {
+  char* p = reinterpret_cast<char*>(head) + at.off * (kBF16 ? 2 : 4);
   if constexpr (kBF16) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_bits(v[2 * i]) | (f32_to_bf16_bits(v[2 * i + 1]) << 16);
-    if (n >= 8) {
+    if (at.n >= 8) {
       __builtin_memcpy(p, w, 16);
     } else if constexpr (!kWhole) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+      if (at.n & 4) {
+        __builtin_memcpy(p, w, 8);
+        p += 8;
+        w[0] = w[2];
+        w[1] = w[3];
+      }
+      if (at.n & 2) {
+        __builtin_memcpy(p, w, 4);
+        p += 4;
+        w[0] = w[1];
+      }
+      if (at.n & 1) *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
     }
   } else {
-    if (n >= 8) {
-      __builtin_memcpy(p, v, 32);
+    typedef float __attribute__((ext_vector_type(4), aligned(4))) f32x4_u;
+    if (at.n >= 8) {
+      *reinterpret_cast<f32x4_u*>(p) = (f32x4_u){v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4_u*>(p + 16) = (f32x4_u){v[4], v[5], v[6], v[7]};
     } else if constexpr (!kWhole) {
+      typedef float __attribute__((ext_vector_type(2), aligned(4))) f32x2_u;
+      const bool four = at.n & 4, pair = at.n & 2;
+      // (values, which the compiler would otherwise choose by their address)
+      float w[7];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) reinterpret_cast<float*>(p)[i] = v[i];
+      for (int i = 0; i < 7; ++i) {
+        w[i] = v[i];
+        asm("" : "+v"(w[i]));
+      }
+      if (four) *reinterpret_cast<f32x4_u*>(p) = (f32x4_u){w[0], w[1], w[2], w[3]};
+      if (pair) *reinterpret_cast<f32x2_u*>(p + 4 * (at.n & 4)) = four ? (f32x2_u){w[4], w[5]} : (f32x2_u){w[0], w[1]};
+      if (at.n & 1)
+        *reinterpret_cast<float*>(p + 4 * (at.n & 6)) = four ? (pair ? w[6] : w[4]) : pair ? w[2] : w[0];
     }
   }
 }
@@ -67,13 +119,7 @@ __device__ __forceinline__ float head_sum(float v, int lanes_log) {
   return v;
 }
 
-// The pieces of a lane: 8 values from off[0] on and 8 from off[1] on, of which
-// n[0] and n[1] exist.
-struct Place {
-  int off[2], n[2];
-};
-
-constexpr int kBatch = 2;        // groups on their way together, and as many behind them
+constexpr int kBatch = 1;        // groups on their way together, and as many behind them
 
 template <bool kBF16, bool kInterleaved, bool kWhole>
 __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lanes_log, int parts) {
@@ -89,17 +135,14 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
   const int j = lane & ((1 << lanes_log) - 1), h_in = lane >> lanes_log;
   const int rl = (p.rot + 15) / 16;                      // lanes that rotate
   const bool rotates = j < rl;
-  Place at;
+  Place at[2];
   if (rotates && !kInterleaved) {
-    at.off[0] = 8 * j;
-    at.off[1] = half + 8 * j;
-    at.n[0] = at.n[1] = min(8, half - 8 * j);
+    at[0] = place(8 * j, half);
+    at[1] = place(half + 8 * j, p.rot);
   } else {
-    const int end = rotates ? p.rot : p.dim;
-    at.off[0] = rotates ? 16 * j : p.rot + 16 * (j - rl);
-    at.off[1] = at.off[0] + 8;
-    at.n[0] = max(0, min(8, end - at.off[0]));
-    at.n[1] = max(0, min(8, end - at.off[1]));
+    const int off = rotates ? 16 * j : p.rot + 16 * (j - rl), end = rotates ? p.rot : p.dim;
+    at[0] = place(off, end);
+    at[1] = place(off + 8, end);
   }
   const int qu = (p.part[0].heads + per - 1) / per, groups = qu + (p.part[1].heads + per - 1) / per;
   const int g0 = groups * part / parts, g1 = groups * (part + 1) / parts;
@@ -115,7 +158,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
       const int h = head(gi) < t.heads ? head(gi) : 0;
       const char* const x = reinterpret_cast<const char*>(t.x) + (b * t.ld + h * t.ld_head) * kSize;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) load8<kBF16, kWhole>(x + at.off[k] * kSize, at.n[k], to[i][k]);
+      for (int k = 0; k < 2; ++k) load8<kBF16, kWhole>(to[i][k], x, at[k]);
     }
   };
   load(in[0], g0);
@@ -147,7 +190,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
     for (int i = 0; i < 2; ++i) {
       if (t.w != nullptr) {
         RowPiece<false> piece;
-        load8<false, kWhole>(t.w + at.off[i], at.n[i], piece);
+        load8<false, kWhole>(piece, t.w, at[i]);
         piece.get(w[i]);
       }
 #pragma unroll
@@ -209,7 +252,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
     if (h < t.heads) {
       char* const o = reinterpret_cast<char*>(t.out) + (b * t.ldo + h * t.ldo_head) * kSize;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) store8<kBF16, kWhole>(o + at.off[i] * kSize, at.n[i], v[i]);
+      for (int i = 0; i < 2; ++i) store8<kBF16, kWhole>(o, at[i], v[i]);
     }
   };
   for (int g = g0; g < g1; g += 2 * kBatch) {
