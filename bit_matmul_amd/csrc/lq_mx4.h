@@ -35,10 +35,10 @@ struct Mx4Gemm {
   bool y_bf16;
 };
 hipError_t launch_mx4_rows(const Mx4Rows& p, hipStream_t stream);
-// How a 4-bit product runs: as Int8Plan.
+// How a 4-bit product runs: the number of its kernel in mx4_gemm.hip's table
+// (the last ones mx4_few.hip's), the rest as Int8Plan.
 struct Mx4Plan {
-  int rows, tokens, ksplit, tiles;
-  bool few;               // mx4_few.hip's kernel
+  int tile, rows, tokens, ksplit, tiles;
   size_t partial_bytes;
 };
 Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus);

@@ -48,7 +48,7 @@ __device__ __forceinline__ f32x4 acc_take(const f32x4& acc) {
 }
 
 template <int PN, int PB, int S, int KB>
-__global__ __launch_bounds__(256, (PN * PB > 4 ? 1 : 2)) void mx4_tile_kernel(
+__global__ __launch_bounds__(256, (PN * PB > 16 || (PN + PB) * KB * S > 2304 ? 1 : 2)) void mx4_tile_kernel(
     Mx4Gemm p, int tiles_n, int tiles_b, int group_n, int ksplit, float* partial) {
   static_assert(S >= 2 && S <= 4 && (KB == 128 || KB == 256), "stages");
   constexpr int kChunks = KB / 16;             // 16-byte chunks, blocks, of a row in a step
@@ -408,23 +408,25 @@ void enqueue_tile(const Mx4Gemm& p, const Mx4Plan& plan, float* partial, hipStre
                        stream, p, tn, tb, group_n, plan.ksplit, partial);
 }
 
-// What the tiles cost in us, as in int8_gemm.hip.
+// The tiles, by their number (launch_mx4_gemm), and what they cost in us, as in
+// int8_gemm.hip.
 struct TileCost {
   int rows, tokens, bytes, per_cu;
   float step, share, ends;
   bool few;
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 128, 1, 1.155f, 0.167f, 3.9f, false}, {224, 256, 128, 1, 0.932f, 0.262f, 3.1f, false},
-    {192, 256, 128, 1, 0.774f, 0.372f, 2.9f, false}, {128, 256, 128, 1, 0.925f, 0.033f, 2.8f, false},
-    {128, 128, 128, 1, 0.469f, 0.058f, 2.6f, false}, {128, 64, 256, 1, 0.829f, 0.013f, 2.2f, false},
-    {64, 128, 256, 1, 0.530f, 0.323f, 2.1f, false},  {64, 64, 256, 2, 0.728f, 0.225f, 1.5f, false},
-    {64, 32, 256, 3, 0.424f, 0.190f, 1.74f, false},  {32, 32, 256, 2, 0.140f, 0.202f, 1.36f, false},
-    {16, 4, 1024, 4, 0.369f, 0.511f, 0.72f, true},   {16, 8, 1024, 3, 0.072f, 0.672f, 0.81f, true},
-    {16, 16, 1024, 2, 0.112f, 0.593f, 1.12f, true},  {32, 16, 1024, 1, 0.007f, 1.171f, 1.45f, true},
+    {256, 256, 128, 1, 0.618f, 1.129f, 8.81f, false}, {224, 256, 128, 1, 0.618f, 0.941f, 9.28f, false},
+    {192, 256, 128, 1, 0.722f, 0.721f, 7.33f, false}, {128, 128, 128, 1, 0.384f, 0.181f, 5.67f, false},
+    {128, 128, 128, 2, 0.413f, 0.338f, 4.64f, false}, {128, 64, 256, 1, 0.651f, 0.056f, 4.84f, false},
+    {128, 64, 128, 1, 0.292f, 0.076f, 4.30f, false}, {64, 64, 128, 2, 0.098f, 0.171f, 4.03f, false},
+    {64, 32, 256, 1, 0.291f, 0.000f, 3.68f, false}, {64, 32, 128, 2, 0.103f, 0.111f, 3.38f, false},
+    {32, 32, 256, 2, 0.154f, 0.111f, 3.49f, false}, {16, 4, 1024, 4, 0.179f, 0.214f, 3.14f, true},
+    {16, 8, 1024, 3, 0.228f, 0.186f, 2.48f, true}, {16, 16, 1024, 2, 0.185f, 0.308f, 2.63f, true},
+    {32, 16, 1024, 1, 0.494f, 0.023f, 2.69f, true},
 };
-constexpr float kJoinUs = 5.0f, kJoinBytesPerUs = 7.0e6f;
-constexpr float kStreamBytesPerUs[2] = {4.72e6f, 6.3e6f}, kHidden[2] = {0.216f, 0.298f};     // tiles, few
+constexpr float kJoinUs = 3.72f, kJoinBytesPerUs = 1.06e+07f;
+constexpr float kStreamBytesPerUs[2] = {7.845e+06f, 1.072e+07f}, kHidden[2] = {0.871f, 1.328f};     // tiles, few
 constexpr int kMaxSplit = 16;
 constexpr int64_t kMaxTiles = 1 << 22;    // (a launch has fewer than 2^32 threads)
 
@@ -457,7 +459,7 @@ Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus) {
       const size_t partial = ks > 1 ? (size_t)units * c.rows * c.tokens * 4 : 0;
       if (ks > 1) us += kJoinUs + 2.0f * (float)partial / kJoinBytesPerUs;
       if (best.rows == 0 || us < best_us) {
-        best = {c.rows, c.tokens, (int)ks, (int)tiles, c.few, partial};
+        best = {(int)(&c - kTiles), c.rows, c.tokens, (int)ks, (int)tiles, partial};
         best_us = us;
       }
     }
@@ -467,19 +469,19 @@ Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus) {
 
 hipError_t launch_mx4_gemm(const Mx4Gemm& p, const Mx4Plan& plan, float* partial, hipStream_t stream) {
   (void)hipGetLastError();   // clear a stale error of an earlier runtime call
-  if (plan.few) return launch_mx4_few(p, plan, stream);
-  switch (plan.rows / 32 * 16 + plan.tokens / 32) {
-    case 0x88: enqueue_tile<8, 8, 2, 128>(p, plan, partial, stream); break;
-    case 0x78: enqueue_tile<7, 8, 2, 128>(p, plan, partial, stream); break;
-    case 0x68: enqueue_tile<6, 8, 2, 128>(p, plan, partial, stream); break;
-    case 0x48: enqueue_tile<4, 8, 2, 128>(p, plan, partial, stream); break;
-    case 0x44: enqueue_tile<4, 4, 4, 128>(p, plan, partial, stream); break;
-    case 0x42: enqueue_tile<4, 2, 3, 256>(p, plan, partial, stream); break;
-    case 0x24: enqueue_tile<2, 4, 3, 256>(p, plan, partial, stream); break;
-    case 0x22: enqueue_tile<2, 2, 2, 256>(p, plan, partial, stream); break;
-    case 0x21: enqueue_tile<2, 1, 2, 256>(p, plan, partial, stream); break;
-    case 0x11: enqueue_tile<1, 1, 4, 256>(p, plan, partial, stream); break;
-    default: return hipErrorInvalidValue;
+  switch (plan.tile) {
+    case 0: enqueue_tile<8, 8, 2, 128>(p, plan, partial, stream); break;
+    case 1: enqueue_tile<7, 8, 2, 128>(p, plan, partial, stream); break;
+    case 2: enqueue_tile<6, 8, 2, 128>(p, plan, partial, stream); break;
+    case 3: enqueue_tile<4, 4, 4, 128>(p, plan, partial, stream); break;
+    case 4: enqueue_tile<4, 4, 2, 128>(p, plan, partial, stream); break;
+    case 5: enqueue_tile<4, 2, 3, 256>(p, plan, partial, stream); break;
+    case 6: enqueue_tile<4, 2, 4, 128>(p, plan, partial, stream); break;
+    case 7: enqueue_tile<2, 2, 4, 128>(p, plan, partial, stream); break;
+    case 8: enqueue_tile<2, 1, 4, 256>(p, plan, partial, stream); break;
+    case 9: enqueue_tile<2, 1, 4, 128>(p, plan, partial, stream); break;
+    case 10: enqueue_tile<1, 1, 4, 256>(p, plan, partial, stream); break;
+    default: return launch_mx4_few(p, plan, stream);
   }
   return hipGetLastError();
 }
