@@ -643,12 +643,11 @@ def lq_mx4_linear(layer: LQMx4Layer, x, B, y, ws=None, gate=None, act=LQ_ACT_NON
            "lq_mx4_linear")
 
 
-def _head_rows(t, name: str, shape, dtype):
+def _head_rows(t, name: str, shape, dtype, device: int):
     """(address, token stride, head stride) of a GPU tensor (tokens, heads, dim)
     whose heads are dense."""
-    # (one test for a call that is right, as _rows)
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and
-            t.get_device() == _current_device()):
+    # (one test for a call that is right, as _rows; a CPU tensor's device is -1)
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device:
         ld, ld_head, step = t.stride()
         if step == 1 or shape[2] == 1:
             return t.data_ptr(), ld, ld_head
@@ -662,28 +661,15 @@ def _head_rows(t, name: str, shape, dtype):
     raise ValueError(f"{name} is on {t.device}, which is not the current device")
 
 
-def _qk_part(x, out, name: str, tokens, dim, dtype):
-    """Addresses, strides and number of the heads of one of the two parts."""
-    if out is None:
-        raise ValueError(f"{name}_out is needed with {name}")
-    shape = x.shape
-    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim:
-        raise ValueError(f"q and k must be (tokens, heads, dim) with the same tokens and dim, {name} is {tuple(shape)}")
-    xp, ld, ld_head = _head_rows(x, name, shape, dtype)
-    op, ldo, ldo_head = (xp, ld, ld_head) if out is x else _head_rows(out, name + "_out", shape, dtype)
-    return xp, op, ld, ld_head, ldo, ldo_head, shape[1]
-
-
 _QK_ARGS = struct.Struct("q4Q8q4Q6ifIQ")
 assert _QK_ARGS.size == ctypes.sizeof(LQQkNormRopeArgs)
 _QK_NORM_ROPE = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, ctypes.c_void_p)(("lq_qk_norm_rope", _lib.LIB))
 _POS_BYTES = {torch.int32: 4, torch.int64: 8}
-_NO_HEADS = (0,) * 7
 
 
-def _flat(t, name: str) -> int:
+def _flat(t, name: str, device: int) -> int:
     """The address of a dense tensor on the current device."""
-    if t.is_cuda and t.is_contiguous() and t.get_device() == _current_device():
+    if t.get_device() == device and t.is_contiguous():
         return t.data_ptr()
     _dev(t, name)
     raise ValueError(f"{name} is on {t.device}, which is not the current device")
@@ -698,29 +684,45 @@ def lq_qk_norm_rope(pos, freq, q=None, k=None, q_out=None, k_out=None, norm=True
     pair of values (the first 2 * freq.numel() values of a head are rotated);
     None: the norm alone."""
     some = k if q is None else q
-    if some is None:
-        raise ValueError("q or k is needed")
-    if some.dim() != 3:
-        raise ValueError("q and k must be GPU tensors of three dimensions")
-    B, _, dim = some.shape
-    dtype = some.dtype
+    if not isinstance(some, torch.Tensor) or not some.is_cuda or some.dim() != 3:
+        raise ValueError("q or k is needed, a GPU tensor of three dimensions")
+    shape = some.shape
+    B, heads, dim = shape
+    dtype, device = some.dtype, _current_device()
     dt = _dtype(some, "k" if q is None else "q")
-    if (q is None and q_out is not None) or (k is None and k_out is not None):
-        raise ValueError("an output without its input")
-    qp, qop, ldq, ldqh, ldqo, ldqoh, q_heads = _NO_HEADS if q is None else _qk_part(q, q_out, "q", B, dim, dtype)
-    kp, kop, ldk, ldkh, ldko, ldkoh, k_heads = _NO_HEADS if k is None else _qk_part(k, k_out, "k", B, dim, dtype)
+    qp = qop = ldq = ldqh = ldqo = ldqoh = q_heads = kp = kop = ldk = ldkh = ldko = ldkoh = k_heads = 0
+    if q is not None:
+        qp, ldq, ldqh = _head_rows(q, "q", shape, dtype, device)
+        qop, ldqo, ldqoh = _head_rows(q_out, "q_out", shape, dtype, device)
+        q_heads = heads
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        if k is not some:
+            shape = k.shape
+            if len(shape) != 3 or shape[0] != B or shape[2] != dim:
+                raise ValueError(f"k has shape {tuple(shape)}, ({B}, heads, {dim}) is needed")
+        kp, ldk, ldkh = _head_rows(k, "k", shape, dtype, device)
+        kop, ldko, ldkoh = _head_rows(k_out, "k_out", shape, dtype, device)
+        k_heads = shape[1]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     rot = pp = fp = 0
     width = 8
-    if freq is not None and freq.numel():
+    if freq is not None:
         rot = 2 * freq.numel()
+    if rot:
         width = _POS_BYTES.get(pos.dtype)
         if width is None or freq.dtype is not torch.float64:
             raise ValueError("pos must be int32 or int64 and freq float64")
         if pos.numel() < B:
             raise ValueError(f"pos must hold {B} positions")
-        pp, fp = _flat(pos, "pos"), _flat(freq, "freq")
-    flags = ((LQ_QK_NORM if norm else 0) | (LQ_QK_ONE_PLUS if one_plus else 0) |
-             (LQ_QK_INTERLEAVED if interleaved else 0))
-    p = _QK_ARGS.pack(B, qp, kp, qop, kop, ldq, ldqh, ldk, ldkh, ldqo, ldqoh, ldko, ldkoh, _vec(w_q, "w_q", dim) or 0,
-                      _vec(w_k, "w_k", dim) or 0, pp, fp, q_heads, k_heads, dim, rot, dt, width, eps, flags, 0)
-    _check(_QK_NORM_ROPE(p, _stream(stream)), "lq_qk_norm_rope")
+        pp, fp = _flat(pos, "pos", device), _flat(freq, "freq", device)
+    flags = (LQ_QK_NORM if norm else 0) | (LQ_QK_ONE_PLUS if one_plus else 0) | (LQ_QK_INTERLEAVED if interleaved else 0)
+    # (packed in the order of the struct's fields, as lq_norm_block)
+    p = _QK_ARGS.pack(B, qp, kp, qop, kop, ldq, ldqh, ldk, ldkh, ldqo, ldqoh, ldko, ldkoh,
+                      0 if w_q is None else _vec(w_q, "w_q", dim), 0 if w_k is None else _vec(w_k, "w_k", dim), pp, fp,
+                      q_heads, k_heads, dim, rot, dt, width, eps, flags, 0)
+    status = _QK_NORM_ROPE(p, _current_stream(device) if stream is None else _stream(stream))
+    if status:
+        _check(status, "lq_qk_norm_rope")
