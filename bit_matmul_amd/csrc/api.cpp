@@ -1393,8 +1393,8 @@ lq_status lq_mx4_linear(const lq_mx4_layer* layer, const void* x, lq_dtype xtype
   const lq::Mx4Rows p =
       mx4_row_args(x, xtype, ldx, gate, ldg, act, B, layer->K, layer->hb, layer->c, q, w.ldq, scale);
   const lq::Mx4Gemm gemm = mx4_args(layer, q, w.ldq, scale, B, y, ytype, ldy);
-  if (const int rows = lq::mx4_token_rows(p, layer->N, w.plan); rows > 0)
-    return hip_status(lq::launch_mx4_token(p, gemm, rows, (hipStream_t)stream));
+  if (lq::mx4_token_fits(p, layer->N, device_cus()))
+    return hip_status(lq::launch_mx4_token(p, gemm, (hipStream_t)stream));
   s = hip_status(lq::launch_mx4_rows(p, (hipStream_t)stream));
   if (s != LQ_OK) return s;
   return hip_status(lq::launch_mx4_gemm(gemm, w.plan,

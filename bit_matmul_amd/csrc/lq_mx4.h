@@ -45,8 +45,8 @@ Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus);
 hipError_t launch_mx4_gemm(const Mx4Gemm& p, const Mx4Plan& plan, float* partial, hipStream_t stream);
 hipError_t launch_mx4_few(const Mx4Gemm& p, const Mx4Plan& plan, hipStream_t stream);
 // Rows and product of one token in one launch (t.q, t.scale and p.q, p.scale
-// unused): the weight rows of a workgroup, 0 where it takes two launches.
-int mx4_token_rows(const Mx4Rows& t, int64_t N, const Mx4Plan& plan);
-hipError_t launch_mx4_token(const Mx4Rows& t, const Mx4Gemm& p, int rows, hipStream_t stream);
+// unused), where it fits.
+bool mx4_token_fits(const Mx4Rows& t, int64_t N, int cus);
+hipError_t launch_mx4_token(const Mx4Rows& t, const Mx4Gemm& p, hipStream_t stream);
 
 }  // namespace lq

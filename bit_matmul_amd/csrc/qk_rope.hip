@@ -23,18 +23,20 @@ struct Place {
 __device__ __forceinline__ Place place(int off, int end) { return {off, max(0, min(8, end - off))}; }
 
 // Loaded at its element's alignment, those that do not exist as zero: 8 at
-// once, or 4, 2 and 1 of them. kWhole: 8 or none.
+// once, or 4, 2 and 1 of them. Pieces hold a multiple of kGrain (8, 4 or 1): what
+// that rules out is left out (777 tokens of 40 + 8 heads of 80, 60 rotated, fp32
+// 12.3 us with all of it, 11.1 with 4).
 typedef uint32_t __attribute__((ext_vector_type(4), aligned(2))) u32x4_u;
 typedef uint32_t __attribute__((ext_vector_type(2), aligned(2))) u32x2_u;
 typedef uint32_t __attribute__((aligned(2))) u32_u;
-template <bool kBF16, bool kWhole>
+template <bool kBF16, int kGrain>
 __device__ __forceinline__ void load8(RowPiece<kBF16>& to, const void* head, const Place& at) {
   const char* const p = reinterpret_cast<const char*>(head) + at.off * (kBF16 ? 2 : 4);
-  const bool four = at.n & 4, pair = at.n & 2, odd = at.n & 1;
+  const bool four = kGrain < 8 && (at.n & 4), pair = kGrain < 4 && (at.n & 2), odd = kGrain < 4 && (at.n & 1);
   if constexpr (kBF16) {
     u32x4_u all = {0, 0, 0, 0};
     if (at.n >= 8) all = *reinterpret_cast<const u32x4_u*>(p);
-    if (!kWhole && at.n < 8) {
+    if (kGrain < 8 && at.n < 8) {
       u32x2_u quad = {0, 0};
       uint32_t two = 0, one = 0;
       if (four) quad = *reinterpret_cast<const u32x2_u*>(p);
@@ -49,7 +51,7 @@ __device__ __forceinline__ void load8(RowPiece<kBF16>& to, const void* head, con
     u32x4_u low = {0, 0, 0, 0}, high = {0, 0, 0, 0};
     if (at.n >= 4) low = *reinterpret_cast<const u32x4_u*>(p);
     if (at.n >= 8) high = *reinterpret_cast<const u32x4_u*>(p + 16);
-    if (!kWhole && at.n < 8) {
+    if (kGrain < 4 && at.n < 8) {
       u32x2_u two = {0, 0};
       uint32_t one = 0;
       if (pair) two = *reinterpret_cast<const u32x2_u*>(p + 4 * (at.n & 4));
@@ -62,7 +64,7 @@ __device__ __forceinline__ void load8(RowPiece<kBF16>& to, const void* head, con
     for (int i = 0; i < 4; ++i) to.w[i] = low[i], to.w[4 + i] = high[i];
   }
 }
-template <bool kBF16, bool kWhole>
+template <bool kBF16, int kGrain>
 __device__ __forceinline__ void store8(void* head, const Place& at, const float (&v)[8]) {
   char* p = reinterpret_cast<char*>(head) + at.off * (kBF16 ? 2 : 4);
   if constexpr (kBF16) {
@@ -71,26 +73,28 @@ __device__ __forceinline__ void store8(void* head, const Place& at, const float 
     for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_bits(v[2 * i]) | (f32_to_bf16_bits(v[2 * i + 1]) << 16);
     if (at.n >= 8) {
       __builtin_memcpy(p, w, 16);
-    } else if constexpr (!kWhole) {
+    } else if constexpr (kGrain < 8) {
       if (at.n & 4) {
         __builtin_memcpy(p, w, 8);
         p += 8;
         w[0] = w[2];
         w[1] = w[3];
       }
-      if (at.n & 2) {
+      if (kGrain < 4 && (at.n & 2)) {
         __builtin_memcpy(p, w, 4);
         p += 4;
         w[0] = w[1];
       }
-      if (at.n & 1) *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+      if (kGrain < 4 && (at.n & 1)) *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
     }
   } else {
     typedef float __attribute__((ext_vector_type(4), aligned(4))) f32x4_u;
     if (at.n >= 8) {
       *reinterpret_cast<f32x4_u*>(p) = (f32x4_u){v[0], v[1], v[2], v[3]};
       *reinterpret_cast<f32x4_u*>(p + 16) = (f32x4_u){v[4], v[5], v[6], v[7]};
-    } else if constexpr (!kWhole) {
+    } else if constexpr (kGrain == 4) {
+      if (at.n & 4) *reinterpret_cast<f32x4_u*>(p) = (f32x4_u){v[0], v[1], v[2], v[3]};
+    } else if constexpr (kGrain < 4) {
       typedef float __attribute__((ext_vector_type(2), aligned(4))) f32x2_u;
       const bool four = at.n & 4, pair = at.n & 2;
       // (values, which the compiler would otherwise choose by their address)
@@ -121,7 +125,7 @@ __device__ __forceinline__ float head_sum(float v, int lanes_log) {
 
 constexpr int kBatch = 1;        // groups on their way together, and as many behind them
 
-template <bool kBF16, bool kInterleaved, bool kWhole>
+template <bool kBF16, bool kInterleaved, int kGrain>
 __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lanes_log, int parts) {
   __shared__ float turns[4][2][kQkMaxDim / 2];
   const int64_t unit = (int64_t)blockIdx.x * 4 + wave_id();
@@ -158,10 +162,18 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
       const int h = head(gi) < t.heads ? head(gi) : 0;
       const char* const x = reinterpret_cast<const char*>(t.x) + (b * t.ld + h * t.ld_head) * kSize;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) load8<kBF16, kWhole>(to[i][k], x, at[k]);
+      for (int k = 0; k < 2; ++k) load8<kBF16, kGrain>(to[i][k], x, at[k]);
     }
   };
+  // (the norms' weights too before the angles: behind them they were a trip to memory more)
+  RowPiece<false> wp[2];
+  auto load_weights = [&](const QkHeads& t) __attribute__((always_inline)) {
+    if (t.w == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load8<false, kGrain>(wp[i], t.w, at[i]);
+  };
   load(in[0], g0);
+  if (p.norm) load_weights(p.part[g0 < qu ? 0 : 1]);
 
   if (half > 0) {
     const double pos = p.pos64 ? (double)reinterpret_cast<const int64_t*>(p.pos)[b]
@@ -184,20 +196,16 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
     s[k] = rotates ? turn[1][min(8 * j + k, half - 1)] : 0.0f;
   }
   float w[2][8];
-  auto weights = [&](const QkHeads& t) __attribute__((always_inline)) {
+  auto take_weights = [&](const QkHeads& t) __attribute__((always_inline)) {
     const float plus = p.one_plus ? 1.0f : 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (t.w != nullptr) {
-        RowPiece<false> piece;
-        load8<false, kWhole>(piece, t.w, at[i]);
-        piece.get(w[i]);
-      }
+      wp[i].get(w[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[i][k] = t.w != nullptr ? plus + w[i][k] : 1.0f;
     }
   };
-  if (p.norm) weights(p.part[g0 < qu ? 0 : 1]);
+  if (p.norm) take_weights(p.part[g0 < qu ? 0 : 1]);
 
   auto one = [&](const RowPiece<kBF16> (&piece)[2], int g) __attribute__((always_inline)) {
     if (g >= g1) return;
@@ -206,7 +214,10 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
 #pragma unroll
     for (int i = 0; i < 2; ++i) piece[i].get(v[i]);
     if (p.norm) {
-      if (g == qu && g != g0) weights(t);
+      if (g == qu && g != g0) {
+        load_weights(t);
+        take_weights(t);
+      }
       float q[2] = {};
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -252,7 +263,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
     if (h < t.heads) {
       char* const o = reinterpret_cast<char*>(t.out) + (b * t.ldo + h * t.ldo_head) * kSize;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) store8<kBF16, kWhole>(o, at[i], v[i]);
+      for (int i = 0; i < 2; ++i) store8<kBF16, kGrain>(o, at[i], v[i]);
     }
   };
   for (int g = g0; g < g1; g += 2 * kBatch) {
@@ -265,16 +276,21 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
   }
 }
 
-template <bool kBF16>
-void enqueue(const QkNormRope& p, bool whole, int lanes_log, int parts, dim3 grid, hipStream_t stream) {
+template <bool kBF16, int kGrain>
+void enqueue(const QkNormRope& p, int lanes_log, int parts, dim3 grid, hipStream_t stream) {
   const dim3 block(256);
-  if (p.interleaved) {
-    if (whole) hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, true, true>), grid, block, 0, stream, p, lanes_log, parts);
-    else hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, true, false>), grid, block, 0, stream, p, lanes_log, parts);
-  } else {
-    if (whole) hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, false, true>), grid, block, 0, stream, p, lanes_log, parts);
-    else hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, false, false>), grid, block, 0, stream, p, lanes_log, parts);
-  }
+  if (p.interleaved)
+    hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, true, kGrain>), grid, block, 0, stream, p, lanes_log, parts);
+  else
+    hipLaunchKernelGGL((qk_norm_rope_kernel<kBF16, false, kGrain>), grid, block, 0, stream, p, lanes_log, parts);
+}
+template <bool kBF16>
+void enqueue(const QkNormRope& p, int lanes_log, int parts, dim3 grid, hipStream_t stream) {
+  // what every piece's values are a multiple of
+  const int all = (p.interleaved ? p.rot : p.rot / 2) | (p.dim - p.rot);
+  if (all % 8 == 0) enqueue<kBF16, 8>(p, lanes_log, parts, grid, stream);
+  else if (all % 4 == 0) enqueue<kBF16, 4>(p, lanes_log, parts, grid, stream);
+  else enqueue<kBF16, 1>(p, lanes_log, parts, grid, stream);
 }
 
 // Wavefronts that keep the device busy.
@@ -289,12 +305,11 @@ hipError_t launch_qk_norm_rope(const QkNormRope& p, hipStream_t stream) {
   while ((1 << lanes_log) < lanes) ++lanes_log;
   const int per = 64 >> lanes_log;
   const int groups = (p.part[0].heads + per - 1) / per + (p.part[1].heads + per - 1) / per;
-  const int64_t want = (kWaves + p.B - 1) / p.B;
-  const int parts = want < groups ? (int)want : groups;
-  const bool whole = p.rot % 16 == 0 && p.dim % 16 == 0;
+  const int64_t want = kWaves / p.B;
+  const int parts = want < 1 ? 1 : want < groups ? (int)want : groups;
   const dim3 grid((unsigned)((p.B * parts + 3) / 4));
-  if (p.bf16) enqueue<true>(p, whole, lanes_log, parts, grid, stream);
-  else enqueue<false>(p, whole, lanes_log, parts, grid, stream);
+  if (p.bf16) enqueue<true>(p, lanes_log, parts, grid, stream);
+  else enqueue<false>(p, lanes_log, parts, grid, stream);
   return hipGetLastError();
 }
 
