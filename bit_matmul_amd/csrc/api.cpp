@@ -1266,10 +1266,12 @@ struct Mx4Ws {
   lq::Mx4Plan plan;
   size_t off_q, off_scale, off_partial, total;
   int64_t ldq;
+  bool token;               // one launch: no plan, no rows
 };
 Mx4Ws mx4_ws(const lq_mx4_layer* l, int64_t B) {
-  Mx4Ws w;
-  w.plan = mx4_plan(l, B);
+  Mx4Ws w{};
+  w.token = lq::mx4_token_fits(B, l->N, l->K, device_cus());
+  if (!w.token) w.plan = mx4_plan(l, B);
   w.ldq = (lq::mx4_row_bytes(l->K) + 127) & ~int64_t(127);     // whole cache lines, as int8_ws
   w.off_q = align_up(lq::kControlBytes);
   w.off_scale = w.off_q + align_up((size_t)B * w.ldq);
@@ -1393,7 +1395,7 @@ lq_status lq_mx4_linear(const lq_mx4_layer* layer, const void* x, lq_dtype xtype
   const lq::Mx4Rows p =
       mx4_row_args(x, xtype, ldx, gate, ldg, act, B, layer->K, layer->hb, layer->c, q, w.ldq, scale);
   const lq::Mx4Gemm gemm = mx4_args(layer, q, w.ldq, scale, B, y, ytype, ldy);
-  if (lq::mx4_token_fits(p, layer->N, device_cus()))
+  if (w.token)
     return hip_status(lq::launch_mx4_token(p, gemm, (hipStream_t)stream));
   s = hip_status(lq::launch_mx4_rows(p, (hipStream_t)stream));
   if (s != LQ_OK) return s;

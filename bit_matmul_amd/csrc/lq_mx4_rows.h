@@ -116,14 +116,16 @@ struct Mx4Block {
     }
   }
 };
+// T: the factor 1 / sqrt(hb) goes into the values, so that sums pass the
+// largest float only where (nearly) a result does.
 __device__ __forceinline__ void mx4_transform(const Mx4Rows& p, float (&v)[2][8]) {
   if (p.lhb == 0) return;
-  fwht_block(v, p.lhb);
-  fwht_restore(v, p.lhb);
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[j][k] *= p.norm;
+  fwht_block(v, p.lhb);
+  fwht_restore(v, p.lhb);
 }
 
 }  // namespace lq

@@ -408,25 +408,31 @@ void enqueue_tile(const Mx4Gemm& p, const Mx4Plan& plan, float* partial, hipStre
                        stream, p, tn, tb, group_n, plan.ksplit, partial);
 }
 
-// The tiles, by their number (launch_mx4_gemm), and what they cost in us, as in
-// int8_gemm.hip.
+// The tiles, by their number (launch_mx4_gemm), and what they cost in us, fitted
+// to 25000 measurements over 1278 sizes (1 to 2048 tokens, 16 to 65536 outputs,
+// 64 to 28672 inputs; some of them in profiles/mx4_product_times.txt): a step
+// takes `step` plus `share` for every workgroup on the compute unit, a
+// workgroup's begin and end take `ends`, and the weights' stream comes on top at
+// its kernel's rate; rows that are no whole cache lines long take kRagged more. Of
+// these sizes the choice is on average 1.0% above the best of these tiles and splits.
+// Left out, with what their absence costs on average: 128 x 256 tokens (0%),
+// 64 x 128 (0.1%), 128 x 64 in 3 steps of 256 bytes (0.1%), 64 x 64 in 2 (0%).
 struct TileCost {
   int rows, tokens, bytes, per_cu;
   float step, share, ends;
   bool few;
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 128, 1, 0.618f, 1.129f, 8.81f, false}, {224, 256, 128, 1, 0.618f, 0.941f, 9.28f, false},
-    {192, 256, 128, 1, 0.722f, 0.721f, 7.33f, false}, {128, 128, 128, 1, 0.384f, 0.181f, 5.67f, false},
-    {128, 128, 128, 2, 0.413f, 0.338f, 4.64f, false}, {128, 64, 256, 1, 0.651f, 0.056f, 4.84f, false},
-    {128, 64, 128, 1, 0.292f, 0.076f, 4.30f, false}, {64, 64, 128, 2, 0.098f, 0.171f, 4.03f, false},
-    {64, 32, 256, 1, 0.291f, 0.000f, 3.68f, false}, {64, 32, 128, 2, 0.103f, 0.111f, 3.38f, false},
-    {32, 32, 256, 2, 0.154f, 0.111f, 3.49f, false}, {16, 4, 1024, 4, 0.179f, 0.214f, 3.14f, true},
-    {16, 8, 1024, 3, 0.228f, 0.186f, 2.48f, true}, {16, 16, 1024, 2, 0.185f, 0.308f, 2.63f, true},
-    {32, 16, 1024, 1, 0.494f, 0.023f, 2.69f, true},
+    {256, 256, 128, 1, 0.257f, 1.406f, 8.80f, false}, {224, 256, 128, 1, 0.381f, 1.138f, 8.79f, false},
+    {192, 256, 128, 1, 0.404f, 0.933f, 8.91f, false}, {128, 128, 128, 1, 0.307f, 0.215f, 5.31f, false},
+    {128, 128, 128, 2, 0.300f, 0.406f, 4.18f, false}, {128, 64, 128, 1, 0.299f, 0.034f, 3.89f, false},
+    {64, 64, 128, 2, 0.080f, 0.160f, 3.71f, false}, {64, 32, 256, 1, 0.291f, 0.000f, 3.81f, false},
+    {64, 32, 128, 2, 0.118f, 0.128f, 3.58f, false}, {32, 32, 256, 2, 0.107f, 0.126f, 3.74f, false},
+    {16, 4, 1024, 4, 0.058f, 0.437f, 2.90f, true}, {16, 8, 1024, 3, 0.145f, 0.265f, 2.36f, true},
+    {16, 16, 1024, 2, 0.214f, 0.312f, 2.88f, true}, {32, 16, 1024, 1, 0.486f, 0.268f, 2.89f, true},
 };
-constexpr float kJoinUs = 3.72f, kJoinBytesPerUs = 1.06e+07f;
-constexpr float kStreamBytesPerUs[2] = {7.845e+06f, 1.072e+07f}, kHidden[2] = {0.871f, 1.328f};     // tiles, few
+constexpr float kJoinUs = 2.31f, kJoinBytesPerUs = 5.83e+06f, kRagged = 0.144f;
+constexpr float kStreamBytesPerUs[2] = {7.579e+06f, 9.369e+06f};     // tiles, few
 constexpr int kMaxSplit = 16;
 constexpr int64_t kMaxTiles = 1 << 22;    // (a launch has fewer than 2^32 threads)
 
@@ -439,6 +445,7 @@ Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus) {
   Mx4Plan best{};
   float best_us = 0.0f;
   const uint32_t bytes = (uint32_t)mx4_row_bytes(K), ucus = (uint32_t)cus;
+  const float ragged = bytes % 128 != 0 ? 1.0f + kRagged : 1.0f;
   for (const TileCost& c : kTiles) {
     if (c.few && (B > c.tokens || (c.tokens > 4 && B <= c.tokens / 2))) continue;   // (no more codes than needed)
     const uint32_t tiles_n = ((uint32_t)N + c.rows - 1) / c.rows, tiles_b = ((uint32_t)B + c.tokens - 1) / c.tokens;
@@ -448,14 +455,13 @@ Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus) {
     uint32_t most = c.few ? 1u : 4u * ucus / tiles;
     most = most < 1u ? 1u : most > (uint32_t)kMaxSplit ? (uint32_t)kMaxSplit : most;
     for (uint32_t ks = 1; ks <= most && ks <= steps; ++ks) {
-      const float len = (float)((steps + ks - 1) / ks);
+      const float len = ragged * (float)((steps + ks - 1) / ks);
       const uint32_t units = tiles * ks, full = units / slots, rem = units - full * slots;
-      float us = (float)full * (len * (c.step + c.share * c.per_cu) + c.ends);
+      float us = ragged * stream + (float)full * (len * (c.step + c.share * c.per_cu) + c.ends);
       if (rem > 0) {
         const float load = 0.5f * ((float)rem / (float)ucus + (float)((rem + ucus - 1) / ucus));
         us += len * (c.step + c.share * load) + c.ends;
       }
-      us = us > stream ? us + kHidden[c.few] * stream : stream + kHidden[c.few] * us;
       const size_t partial = ks > 1 ? (size_t)units * c.rows * c.tokens * 4 : 0;
       if (ks > 1) us += kJoinUs + 2.0f * (float)partial / kJoinBytesPerUs;
       if (best.rows == 0 || us < best_us) {
@@ -475,12 +481,11 @@ hipError_t launch_mx4_gemm(const Mx4Gemm& p, const Mx4Plan& plan, float* partial
     case 2: enqueue_tile<6, 8, 2, 128>(p, plan, partial, stream); break;
     case 3: enqueue_tile<4, 4, 4, 128>(p, plan, partial, stream); break;
     case 4: enqueue_tile<4, 4, 2, 128>(p, plan, partial, stream); break;
-    case 5: enqueue_tile<4, 2, 3, 256>(p, plan, partial, stream); break;
-    case 6: enqueue_tile<4, 2, 4, 128>(p, plan, partial, stream); break;
-    case 7: enqueue_tile<2, 2, 4, 128>(p, plan, partial, stream); break;
-    case 8: enqueue_tile<2, 1, 4, 256>(p, plan, partial, stream); break;
-    case 9: enqueue_tile<2, 1, 4, 128>(p, plan, partial, stream); break;
-    case 10: enqueue_tile<1, 1, 4, 256>(p, plan, partial, stream); break;
+    case 5: enqueue_tile<4, 2, 4, 128>(p, plan, partial, stream); break;
+    case 6: enqueue_tile<2, 2, 4, 128>(p, plan, partial, stream); break;
+    case 7: enqueue_tile<2, 1, 4, 256>(p, plan, partial, stream); break;
+    case 8: enqueue_tile<2, 1, 4, 128>(p, plan, partial, stream); break;
+    case 9: enqueue_tile<1, 1, 4, 256>(p, plan, partial, stream); break;
     default: return launch_mx4_few(p, plan, stream);
   }
   return hipGetLastError();

@@ -166,9 +166,9 @@ __global__ __launch_bounds__(64 * W) void mx4_token_kernel(Mx4Rows t, Mx4Gemm p)
 // One token, a row of at most 16384 values, 8 at a time, and of more than 8192
 // only where every 16 rows have a compute unit: LDS holds no more of those, and the row would be
 // made again for each (14336 -> 4096 with a gate 10.9 us, in two launches 11.1).
-bool mx4_token_fits(const Mx4Rows& t, int64_t N, int cus) {
-  if (t.B != 1 || t.K % 8 != 0 || N > (int64_t(1) << 26)) return false;
-  return t.K <= 8192 || (t.K <= 16384 && (N + 15) / 16 <= cus);
+bool mx4_token_fits(int64_t B, int64_t N, int64_t K, int cus) {
+  if (B != 1 || K % 8 != 0 || N > (int64_t(1) << 26)) return false;
+  return K <= 8192 || (K <= 16384 && (N + 15) / 16 <= (cus > 0 ? cus : 256));
 }
 
 template <bool kXBF16, bool kGate, bool kScaled>
