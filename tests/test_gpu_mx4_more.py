@@ -263,6 +263,49 @@ def test_rows_behind_the_last_one_stay(lq, B):
     assert torch.all(y[B:] == 4.0) and torch.all(y[:B] != 4.0)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N,K,hb", [(1, 8, 1), (33, 40, 8), (300, 2040, 1), (90, 2048, 1024), (16, 3000, 1), (300, 4096, 512),
+                                    (77, 8192, 1024), (4100, 8000, 64), (130, 8200, 1), (2000, 14336, 1024), (4096, 16384, 128)])
+def test_one_token_in_one_launch(lq, N, K, hb, dtype):
+    """Every length of row that one launch takes, with a gate, T, a row scale and a bias and without: no rows in the
+    workspace, and the product of lq_mx4_quant_rows' rows."""
+    rng = np.random.default_rng(N + K)
+    c = (0.8 + 0.4 * torch.rand(K, generator=torch.Generator().manual_seed(3))).to(DEV) if hb > 1 else None
+    for act in (None, "gelu"):
+        lay = Layer(lq, N, K, bias=act is None, row_scale=act is not None, hb=hb, c=c)
+        x, g = randn(rng, 1, K).to(dtype), randn(rng, 1, K).to(dtype)
+        y = torch.full((2, N), 4.0, dtype=dtype, device=DEV)
+        ws = workspace(lq.lq_mx4_linear_workspace_size(lay.struct, 1, dtype))
+        how = dict(gate=g, act=lq.LQ_ACT_GELU) if act else {}
+        note(f"lq_mx4_linear one token N={N} K={K} hb={hb} {dtype} act={act}")
+        lq.lq_mx4_linear(lay.struct, x, 1, y, ws, **how)
+        torch.cuda.synchronize()
+        assert torch.all(ws == 0xA5) and torch.all(y[1] == 4.0)
+        code, scale = quant(lq, x, gate=g if act else None, act=act or "none", hb=hb, c=c)
+        near_product(y[:1], ref.decode(code, scale, K), lay)
+
+
+@pytest.mark.parametrize("N,K", [(40, 4099), (4112, 8200), (40, 20000)])
+def test_one_token_in_two_launches(lq, N, K):
+    """Rows not 8 values at a time, too long, or with more outputs than compute units take."""
+    rng = np.random.default_rng(K)
+    lay, x = Layer(lq, N, K), randn(rng, 1, K)
+    y, ws = torch.empty(1, N, device=DEV), workspace(lq.lq_mx4_linear_workspace_size(lay.struct, 1, F32))
+    lq.lq_mx4_linear(lay.struct, x, 1, y, ws)
+    torch.cuda.synchronize()
+    assert not torch.all(ws == 0xA5)
+    near_product(y, ref.decode(*quant(lq, x), K), lay)
+
+
+def test_one_token_holding_an_infinity(lq):
+    lay, x = Layer(lq, 100, 4096), torch.ones(1, 4096, device=DEV)
+    y = torch.zeros(1, 100, device=DEV)
+    x[0, 77] = float("inf")
+    lq.lq_mx4_linear(lay.struct, x, 1, y, workspace(lq.lq_mx4_linear_workspace_size(lay.struct, 1, F32)))
+    torch.cuda.synchronize()
+    assert torch.isnan(y).all()
+
+
 def far_rows(rows, cols, dtype, ld):
     return torch.empty(rows * ld, dtype=dtype, device=DEV).view(rows, ld)[:, :cols]
 
