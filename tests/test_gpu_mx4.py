@@ -160,7 +160,7 @@ def near_codes(got, v, off):
 @pytest.mark.parametrize("hb", [2, 4, 8, 16, 32, 64, 128, 256, 512, 1024])
 def test_quant_rows_transform(lq, hb, dtype):
     rng = np.random.default_rng(hb)
-    K = 3 * 1024 if hb == 1024 else hb * (5 * 1024 // hb // 2 + 1)
+    K = hb * (5 if hb >= 512 else 5 * 1024 // hb // 2 + 1)
     x = randn(rng, 5, K).to(dtype)
     c = 0.8 + 0.4 * torch.rand(K, generator=torch.Generator().manual_seed(hb)).to(DEV)
     got = quant(lq, x, hb=hb, c=c)
