@@ -1,5 +1,5 @@
-// The microscaled 4-bit layers' arguments and launches (arguments as in
-// include/lq.h), and device helpers of their kernels.
+// The microscaled 4-bit layers' sizes, arguments and launches (arguments as in
+// include/lq.h).
 #pragma once
 
 #include "lq_8bit.h"

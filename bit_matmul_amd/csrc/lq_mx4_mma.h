@@ -1,4 +1,4 @@
-// Device helpers of the 4-bit products (mx4_gemm.hip, mx4_few.hip).
+// Device helpers of the 4-bit products (mx4_gemm.hip, mx4_few.hip, mx4_token.hip).
 #pragma once
 
 #include "lq_int8.h"

@@ -1,5 +1,6 @@
-// Device helpers of the row kernels (quant_rows.hip, norm_block.hip, mx4_rows.hip): one
-// workgroup holds one row of K values in registers. Device-only.
+// Device helpers of the row kernels (quant_rows.hip, norm_block.hip): one
+// workgroup holds one row of K values in registers. Parts of them serve
+// mx4_rows.hip, mx4_token.hip, qk_rope.hip and int8_token.hip. Device-only.
 //
 // Layout: the row is cut into blocks of 1024 values; wavefront w of W takes
 // blocks w, w + W, ... (C of them). Of a block, lane l holds the values
