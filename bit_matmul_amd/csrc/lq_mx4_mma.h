@@ -29,19 +29,18 @@ __device__ __forceinline__ uint32_t mx4_scale_mask(int left, int i) {
   return m;
 }
 
-// The scales and biases of rows n .. n + 3 (rows past N as the last one; none: 1 and 0).
+// The scales and biases of rows n .. n + 3 (rows past N as the last one; none: 1
+// and 0), all of them on their way at once.
 __device__ __forceinline__ void load_mx4_rows(const Mx4Gemm& p, int64_t n, float (&rs)[4], float (&bias)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) rs[e] = 1.0f, bias[e] = 0.0f;
-  if (n + 4 <= p.N) {
-    if (p.row_scale != nullptr) __builtin_memcpy(rs, p.row_scale + n, 16);
-    if (p.bias != nullptr) __builtin_memcpy(bias, p.bias + n, 16);
-    return;
-  }
+  if (p.row_scale != nullptr) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (p.row_scale != nullptr) rs[e] = p.row_scale[min(n + e, p.N - 1)];
-    if (p.bias != nullptr) bias[e] = p.bias[min(n + e, p.N - 1)];
+    for (int e = 0; e < 4; ++e) rs[e] = p.row_scale[min(n + e, p.N - 1)];
+  }
+  if (p.bias != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bias[e] = p.bias[min(n + e, p.N - 1)];
   }
 }
 

@@ -129,6 +129,12 @@ __global__ __launch_bounds__(256) void mx4_few_kernel(Mx4Gemm p) {
       for (int i = 0; i < kPanels; ++i) acc[i] = mfma_mx4<1>(a[i][2 * u + 1], c[2 * u + 1], acc[i], sa[i][u], sc[u]);
     }
   };
+  // Wavefront i adds up and stores panel i: lane (g, r) holds weight rows
+  // 4 g .. 4 g + 3 for token r. Their scales and biases are on their way from here on.
+  const int64_t n = n0 + 16 * (wave % kPanels) + 4 * g;
+  float rs[4], bias[4];
+  load_mx4_rows(p, n, rs, bias);
+  __builtin_amdgcn_sched_barrier(0);
   copy_step(s0, stage0);
   copy_step(s0 + 1, stage1);
   int s = s0;
@@ -146,12 +152,7 @@ __global__ __launch_bounds__(256) void mx4_few_kernel(Mx4Gemm p) {
 #pragma unroll
   for (int i = 0; i < kPanels; ++i) meet[(4 * i + wave) * 64 + lane] = acc[i];
   __syncthreads();
-  // Wavefront i adds up and stores panel i: lane (g, r) holds weight rows
-  // 4 g .. 4 g + 3 for token r.
-  const int64_t n = n0 + 16 * wave + 4 * g;
   if (wave >= kPanels || n >= p.N || r >= tokens) return;
-  float rs[4], bias[4];
-  load_mx4_rows(p, n, rs, bias);
   f32x4 sum = meet[4 * wave * 64 + lane];
 #pragma unroll
   for (int k = 1; k < 4; ++k) sum += meet[(4 * wave + k) * 64 + lane];

@@ -79,6 +79,7 @@ __global__ __launch_bounds__(256, (PN * PB > 16 || (PN + PB) * KB * S > 2304 ? 1
   __shared__ uint4 stage1[kStage];
   __shared__ uint4 stage2[S > 2 ? kStage : 1];
   __shared__ uint4 stage3[S > 3 ? kStage : 1];
+  __shared__ __attribute__((aligned(16))) float outs[2][256];         // the rows' scales and biases
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int g = lane >> 4, r = lane & 15;
   const int wn = wave & 1, wb = wave >> 1;
@@ -198,6 +199,12 @@ __global__ __launch_bounds__(256, (PN * PB > 16 || (PN + PB) * KB * S > 2304 ? 1
       asm("" : "+a"(acc[i][j]));
     }
 
+  // The rows' scales and biases, here: behind the loop they were one trip to
+  // memory after another. (Threads past the tile's rows: the last row's.)
+  const int64_t out = min(n0 + (int)threadIdx.x, p.N - 1);
+  const float out_scale = p.row_scale != nullptr ? p.row_scale[out] : 1.0f;
+  const float out_bias = p.bias != nullptr ? p.bias[out] : 0.0f;
+  __builtin_amdgcn_sched_barrier(0);
   copy_step(s0, stage0);
   copy_step(s0 + 1, stage1);
   if constexpr (S > 2) copy_step(s0 + 2, stage2);
@@ -324,12 +331,18 @@ __global__ __launch_bounds__(256, (PN * PB > 16 || (PN + PB) * KB * S > 2304 ? 1
       for (int j = 0; j < PB; ++j) o[(i * PB + j) * 64] = acc[i][j];
     return;
   }
-  // (scales first, pairs of panels exchanged so that a token's four lanes store
+  outs[0][threadIdx.x] = out_scale;
+  outs[1][threadIdx.x] = out_bias;
+  lds_barrier();
+  // (pairs of panels exchanged so that a token's four lanes store
   // 64 consecutive bytes: int8_gemm.hip)
   const int64_t nw = n0 + 16 * wn * PN, bw = b0 + 16 * wb * PB + r;
   float rs[PN][4], bias[PN][4];
 #pragma unroll
-  for (int i = 0; i < PN; ++i) load_mx4_rows(p, min(nw + 16 * i + 4 * g, p.N - 1), rs[i], bias[i]);
+  for (int i = 0; i < PN; ++i) {
+    __builtin_memcpy(rs[i], &outs[0][16 * (wn * PN + i) + 4 * g], 16);
+    __builtin_memcpy(bias[i], &outs[1][16 * (wn * PN + i) + 4 * g], 16);
+  }
   if (p.y_bf16 && nw + 16 * PN <= p.N) {
 #pragma unroll
     for (int j = 0; j < PB; ++j) {
