@@ -630,7 +630,8 @@ lq_status lq_mx4_gemm_plan(const lq_mx4_layer* layer, int64_t B, lq_mx4_plan_inf
 /*
  * The whole 4-bit layer of act(gate) .* x: lq_mx4_quant_rows with the layer's
  * T, then lq_mx4_gemm, the 4-bit rows in the workspace (behind its control
- * area, which is left as it is). gate NULL: x alone. Errors: as those two.
+ * area, which is left as it is). gate NULL: x alone. y overlaps no input, and
+ * the workspace nothing. Errors: as those two.
  */
 lq_status lq_mx4_linear_workspace_size(const lq_mx4_layer* layer, int64_t B, lq_dtype xtype,
                                        size_t* bytes);
