@@ -7,12 +7,12 @@
 // they meet once, at the end. With each step come the scales of 512 values: 256
 // bytes of a panel, which lie together in memory, a copy of 4 bytes a lane.
 //
-// Bound by the weights' stream: 16 tokens 28672 -> 8192 24.5 us (5.1 TB/s, its launch
-// included; tiles and a join 28), 4 tokens 23.4, 8 tokens 8192 -> 28672 26.9 (4.6). One
+// Bound by the weights' stream: 16 tokens 28672 -> 8192 24.2 us (5.2 TB/s, its launch
+// included; tiles and a join 28), 4 tokens 23.3, 8 tokens 8192 -> 28672 27.2 (4.6). One
 // panel to a workgroup, so that two to four of them share a compute unit and one
 // copies while another multiplies; two panels, where 16 tokens' codes would
 // be as many bytes as one panel's weights. A third stage was slower (16 tokens 24.5 ->
-// 25.1, 8 tokens 26.9 -> 29.6): fewer workgroups to a compute unit.
+// 25.1 us, 8 tokens 26.9 -> 29.6): fewer workgroups to a compute unit.
 #include <type_traits>
 
 #include "lq_mx4_mma.h"

@@ -16,13 +16,14 @@
 //
 // Sums are the instruction's own, fp32, over 128 values and then in order.
 //
-// 2048 tokens 8192 -> 28672 238 us (4.04 PFLOP/s), 28672 -> 8192 198 (4.86). Bound
-// by the copies: alone, without products, they take 179 of those 198 us, products
+// 2048 tokens 8192 -> 28672 230 us (4.18 PFLOP/s), 28672 -> 8192 192 (5.0). Bound by
+// the copies: alone, without products, they take 179 of those 192 us, products
 // and reads of LDS alone 127; a compute unit holds one such workgroup, and LDS two
 // stages of its tiles, so a copy has one step, 1.7 us, to arrive. Larger tiles than
 // 256 x 256 have no registers for their sums, smaller ones copy more for a product
 // (20480 -> 8192 174 us; in 128 x 128, two to a compute unit, 191, in four
-// stages 223). 64 tokens 5120 -> 27648 15.8 us, its 75 MB of weights at 4.8 TB/s.
+// stages 223), and copies of 64 bytes of a row, four stages of them, ask L2 twice as
+// often (218). 64 tokens 5120 -> 27648 15.3 us, its 75 MB of weights at 4.9 TB/s.
 #include <type_traits>
 
 #include "lq_mx4_mma.h"
