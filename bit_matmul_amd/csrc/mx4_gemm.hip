@@ -16,14 +16,16 @@
 //
 // Sums are the instruction's own, fp32, over 128 values and then in order.
 //
-// 2048 tokens 8192 -> 28672 230 us (4.18 PFLOP/s), 28672 -> 8192 192 (5.0). Bound by
-// the copies: alone, without products, they take 179 of those 192 us, products
-// and reads of LDS alone 127; a compute unit holds one such workgroup, and LDS two
-// stages of its tiles, so a copy has one step, 1.7 us, to arrive. Larger tiles than
-// 256 x 256 have no registers for their sums, smaller ones copy more for a product
-// (20480 -> 8192 174 us; in 128 x 128, two to a compute unit, 191, in four
-// stages 223), and copies of 64 bytes of a row, four stages of them, ask L2 twice as
-// often (218). 64 tokens 5120 -> 27648 15.3 us, its 75 MB of weights at 4.9 TB/s.
+// 2048 tokens 8192 -> 28672 230 us (4.18 PFLOP/s), 28672 -> 8192 192 (5.0), of which
+// the matrix cores are busy for 57%, LDS (operands read twice over, copies
+// written) for about half. Copies without products take 179 us, products and reads
+// without copies 127; codes of nothing but zeros, which cost less power, 12% less.
+// One wavefront on a SIMD issues all of it in turn: what gave the copies more time
+// was slower (stages of 64 bytes, four of them, 192 -> 210; copies issued half a step
+// earlier, with a second barrier, 204 -> 232), and so were smaller tiles, which copy
+// more for a product (20480 -> 8192 174 us; in 128 x 128, two to a compute unit, 191,
+// in four stages 223). Larger ones than 256 x 256 have no registers for their sums.
+// 64 tokens 5120 -> 27648 15.3 us, its 75 MB of weights at 4.9 TB/s.
 #include <type_traits>
 
 #include "lq_mx4_mma.h"
