@@ -1301,6 +1301,7 @@ lq::Mx4Rows mx4_row_args(const void* x, lq_dtype xtype, int64_t ldx, const void*
                          int64_t ldq, uint8_t* scale) {
   lq::Mx4Rows p{x, gate, c, q, scale, B, K, ldx, ldg, ldq, (int)act, 0, 1.0f, xtype == LQ_BF16};
   fill_hb(&p, hb);
+  p.norm = ldexpf(1.0f, -((p.lhb + 1) / 2));   // (the sqrt(2) of an odd one: mx4_transform)
   return p;
 }
 

@@ -20,7 +20,7 @@ struct Mx4Rows {
   uint8_t* scale;
   int64_t B, K, ldx, ldg, ldq;
   int act, lhb;
-  float norm;            // 1 / sqrt(hb)
+  float norm;            // 2^-ceil(lhb / 2)
   bool x_bf16;           // x and gate
 };
 struct Mx4Gemm {

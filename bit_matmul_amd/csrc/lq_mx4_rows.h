@@ -116,8 +116,10 @@ struct Mx4Block {
     }
   }
 };
-// T: the factor 1 / sqrt(hb) goes into the values, so that sums pass the
-// largest float only where (nearly) a result does.
+// T: of the factor 1 / sqrt(hb) the power of two 2^-ceil(log2(hb) / 2) goes into the
+// values, exactly, so that sums pass the largest float only where (nearly) a result does,
+// and the sqrt(2) that an odd log2 hb leaves multiplies the results, one rounding of each.
+// (1 / sqrt(128) itself in front rounded every one of 128 inputs.)
 __device__ __forceinline__ void mx4_transform(const Mx4Rows& p, float (&v)[2][8]) {
   if (p.lhb == 0) return;
 #pragma unroll
@@ -125,6 +127,12 @@ __device__ __forceinline__ void mx4_transform(const Mx4Rows& p, float (&v)[2][8]
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[j][k] *= p.norm;
   fwht_block(v, p.lhb);
+  if (p.lhb & 1) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[j][k] *= 1.41421356237309504880f;
+  }
   fwht_restore(v, p.lhb);
 }
 
