@@ -652,8 +652,9 @@ lq_status lq_mx4_linear(const lq_mx4_layer* layer, const void* x, lq_dtype xtype
  *         j = i + rot / 2; with LQ_QK_INTERLEAVED the pairs are (u_2i, u_2i+1)
  *     u_k for k >= rot stay as they are
  *
- * in fp32, rounded once to dtype; angles are reduced in fp64, so that far
- * positions keep their accuracy (the angle is off by 2^-51 of itself and 1e-7).
+ * in fp32, rounded once to dtype; cos and sin are taken in fp64 and rounded once
+ * to fp32, so that far positions keep their accuracy (the angle is off by 2^-51 of
+ * itself).
  * NULL w: all ones. LQ_QK_ONE_PLUS: 1 + w in place of w. rot == 0: the norm alone. Element k of
  * head h of token b lies at b ld + h ld_head + k: heads side by side in a row,
  * or one after the other. q_out may be q and k_out k, with the same ld and ld_head;
