@@ -710,9 +710,11 @@ def lq_qk_norm_rope(pos, freq, q=None, k=None, q_out=None, k_out=None, norm=True
     rot = pp = fp = 0
     width = 8
     if freq is not None:
+        if not isinstance(freq, torch.Tensor):
+            raise ValueError("freq must be a float64 tensor")
         rot = 2 * freq.numel()
     if rot:
-        width = _POS_BYTES.get(pos.dtype)
+        width = _POS_BYTES.get(getattr(pos, "dtype", None))
         if width is None or freq.dtype is not torch.float64:
             raise ValueError("pos must be int32 or int64 and freq float64")
         if pos.numel() < B:
