@@ -252,8 +252,10 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[i] = fmaf(v[i][k], v[i][k], q[i]);
       const float sum = head_sum(q[0] + q[1], lanes_log);
-      float r = inv_root(sum / (float)p.dim + p.eps);
-      if (__builtin_amdgcn_ballot_w64(!(sum <= 3.0e38f)) != 0) {
+      const float mean = sum / (float)p.dim + p.eps;
+      float r = inv_root(mean);
+      // (the sum, or it and a large eps, passes the largest float)
+      if (__builtin_amdgcn_ballot_w64(!(sum <= 3.0e38f && mean <= 3.4e38f)) != 0) {
         // (as norm_block.hip: squares of v 2^-80, half of that factor into v)
         float z = 0.0f;
 #pragma unroll
@@ -264,7 +266,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope p, int lan
             z = fmaf(u, u, z);
           }
         z = head_sum(z, lanes_log);
-        if (!(sum <= 3.0e38f)) {
+        if (!(sum <= 3.0e38f && mean <= 3.4e38f)) {
           r = inv_root(z / (float)p.dim + p.eps * 0x1p-80f * 0x1p-80f) * 0x1p-40f;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
