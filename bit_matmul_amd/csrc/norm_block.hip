@@ -42,8 +42,8 @@ __device__ __forceinline__ float sum_squares(float (&v)[C][2][8], F f) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// 1 / sqrt(mean(v^2) + eps). Where the sum of squares passes the largest
-// float, it is taken again of v 2^-80 (every thread of the workgroup sees the
+// 1 / sqrt(mean(v^2) + eps). Where the sum of squares, or the mean's with a large
+// eps, passes the largest float, it is taken again of v 2^-80 (every thread of the workgroup sees the
 // same sum, so all take the branch together), with eps 2^-160 (0 below 2^11,
 // which is nothing next to a mean of 4.6e33 or more). The root is then 2^80
 // times too large, and half of that factor goes into v: the norm stays what it
@@ -52,7 +52,8 @@ __device__ __forceinline__ float sum_squares(float (&v)[C][2][8], F f) {
 template <int C>
 __device__ __forceinline__ float inv_rms(float (&v)[C][2][8], int K, float eps, float* red) {
   float s = row_reduce<SumF>(sum_squares<C>(v, [](float& u) { return u; }), red);
-  if (s <= 3.0e38f) return inv_root(s / (float)K + eps);
+  const float mean = s / (float)K + eps;
+  if (s <= 3.0e38f && mean <= 3.4e38f) return inv_root(mean);
   s = row_reduce<SumF>(sum_squares<C>(v, [](float& u) { return (u *= 0x1p-40f) * 0x1p-40f; }),
                        red + kRowMaxWaves);
   return inv_root(s / (float)K + eps * 0x1p-80f * 0x1p-80f) * 0x1p-40f;
