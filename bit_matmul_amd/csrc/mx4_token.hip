@@ -50,6 +50,8 @@ __global__ __launch_bounds__(64 * W) void mx4_token_kernel(Mx4Rows t, Mx4Gemm p)
 #pragma unroll
   for (int i = 0; i < kC; ++i)
     in[i].load(t, reinterpret_cast<const char*>(t.x), reinterpret_cast<const char*>(t.gate), col0(i));
+  // (Loads and copies are counted below: in this order.)
+  __builtin_amdgcn_sched_barrier(0);
   const uint8_t* const wbase = p.w + n0 * p.ldw;
   const uint8_t* const sbase = p.w_scale + (int64_t)blockIdx.x * ((int64_t)units * 128) + 4 * (lane & 31);
   auto copy_step = [&](int i, uint4* stage) __attribute__((always_inline)) {
