@@ -1268,9 +1268,9 @@ struct Mx4Ws {
   int64_t ldq;
   bool token;               // one launch: no plan, no rows
 };
-Mx4Ws mx4_ws(const lq_mx4_layer* l, int64_t B) {
+Mx4Ws mx4_ws(const lq_mx4_layer* l, int64_t B, bool gate) {
   Mx4Ws w{};
-  w.token = lq::mx4_token_fits(B, l->N, l->K, device_cus());
+  w.token = lq::mx4_token_fits(B, l->N, l->K, device_cus(), l->hb > 1, gate);
   if (!w.token) w.plan = mx4_plan(l, B);
   w.ldq = (lq::mx4_row_bytes(l->K) + 127) & ~int64_t(127);     // whole cache lines, as int8_ws
   w.off_q = align_up(lq::kControlBytes);
@@ -1374,7 +1374,8 @@ lq_status lq_mx4_linear_workspace_size(const lq_mx4_layer* layer, int64_t B, lq_
   if (bytes == nullptr || !valid_dtype(xtype)) return LQ_ERR_INVALID_ARG;
   lq_status s = check_mx4_layer(layer, B);
   if (s != LQ_OK) return s;
-  *bytes = B == 0 || layer->N == 0 ? 0 : mx4_ws(layer, B).total;
+  // (a call with a gate needs as much as one without, or more)
+  *bytes = B == 0 || layer->N == 0 ? 0 : mx4_ws(layer, B, true).total;
   return LQ_OK;
 }
 
@@ -1385,7 +1386,7 @@ lq_status lq_mx4_linear(const lq_mx4_layer* layer, const void* x, lq_dtype xtype
   lq_status s = check_mx4_layer(layer, B);
   if (s != LQ_OK) return s;
   if (B == 0 || layer->N == 0) return LQ_OK;
-  const Mx4Ws w = mx4_ws(layer, B);
+  const Mx4Ws w = mx4_ws(layer, B, gate != nullptr);
   s = check_row_inputs(x, xtype, ldx, gate, ldg, layer->c, layer->K);
   if (s == LQ_OK) s = check_mx4_ptrs(layer, y, ytype, ldy);
   if (s == LQ_OK) s = check_ws(ws, ws_bytes, w.total);

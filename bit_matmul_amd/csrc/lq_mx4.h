@@ -45,8 +45,8 @@ Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus);
 hipError_t launch_mx4_gemm(const Mx4Gemm& p, const Mx4Plan& plan, float* partial, hipStream_t stream);
 hipError_t launch_mx4_few(const Mx4Gemm& p, const Mx4Plan& plan, hipStream_t stream);
 // Rows and product of one token in one launch (t.q, t.scale and p.q, p.scale
-// unused), where it fits.
-bool mx4_token_fits(int64_t B, int64_t N, int64_t K, int cus);
+// unused), where it fits and is faster than two.
+bool mx4_token_fits(int64_t B, int64_t N, int64_t K, int cus, bool transform, bool gate);
 hipError_t launch_mx4_token(const Mx4Rows& t, const Mx4Gemm& p, hipStream_t stream);
 
 }  // namespace lq

@@ -3,17 +3,18 @@
 //
 // int8_token.hip's form: the row is loaded first, then all of the weights are
 // on their way to LDS before the codes are made; products as in mx4_few.hip,
-// each of the W wavefronts its part of the reduction alone, S steps of 256 bytes
-// at most. Every lane of a token's column reads the same 16 bytes of codes, so
-// all 16 columns of a product hold the token's sums, and what the wavefronts meet
-// with is 64 bytes each.
+// each of the W wavefronts 1024 values of the row and its part of the reduction
+// alone, one step of 256 bytes or two. Every lane of a token's column reads the same 16
+// bytes of codes, so all 16 columns of a product hold the token's sums, and what the
+// wavefronts meet with is 64 bytes each.
 //
-// In replays of a graph, weights from memory: 8192 -> 10240 11.2 us (4.0 TB/s with
-// its launch; in two launches 13.9), with T, which every workgroup makes again, 14.2
-// (14.5); 8192 -> 28672 22.8 (26.0; 5.5 TB/s); 4096 -> 14336 7.7; 14336 -> 4096 8.7, with a
-// gate 10.9; 512 -> 512 2.4 (4.3). One workgroup for each compute unit, which
-// makes the codes once and goes on from panel to panel through two buffers, was no
-// faster (8192 -> 10240 12.4, with T 13.4; 28672 25.6): fewer wavefronts have less on
+// In replays of a graph, weights from memory: 8192 -> 10240 10.8 us (4.1 TB/s with
+// its launch; in two launches 13.1), with T, which every workgroup makes again, 12.1
+// (13.8), with T and a gate 14.4 (14.7); 8192 -> 28672 23.2 (31.1); 14336 -> 4096 8.4 (10.2),
+// with a gate 9.5 (11.0; 8 wavefronts of two blocks of 1024 values each took 10.7); 512 -> 1024
+// 3.1 (4.7). One workgroup for each compute unit, which makes the codes once and goes on
+// from panel to panel through two buffers, was no faster (8192 -> 10240 12.4, with T 13.4;
+// 28672 25.6, where this form took 11.2, 14.2 and 22.8): fewer wavefronts have less on
 // their way.
 #include <type_traits>
 
@@ -27,12 +28,10 @@ template <bool kXBF16, bool kGate, bool kScaled, int W, int S>
 __global__ __launch_bounds__(64 * W) void mx4_token_kernel(Mx4Rows t, Mx4Gemm p) {
   constexpr int kCopies = 4 + 1;                                   // of codes, 4 rows, 1 KB, each, and of scales, 256 bytes
   constexpr int kSize = 4 * 64 + 16;                               // 16-byte units of a wavefront's step
-  constexpr int kC = (S + 1) / 2;                                  // blocks of 1024 values to a wavefront
+  static_assert(S == 1 || S == 2, "steps: 1024 values of the row to a wavefront");
   // (an array for each step: of one the compiler would await all copies before it reads the first)
   __shared__ uint4 stage0[W * kSize];
   __shared__ uint4 stage1[S > 1 ? W * kSize : 1];
-  __shared__ uint4 stage2[S > 2 ? W * kSize : 1];
-  __shared__ uint4 stage3[S > 3 ? W * kSize : 1];
   __shared__ uint4 codes[W * S * 16];
   __shared__ uint16_t scales[W * S * 8];                           // of a 256: 4 of two blocks each
   __shared__ __attribute__((aligned(16))) float meet[W * 16];
@@ -45,11 +44,9 @@ __global__ __launch_bounds__(64 * W) void mx4_token_kernel(Mx4Rows t, Mx4Gemm p)
   const int rows = (int)min((int64_t)16, p.N - n0);
 
   // ---- the row's loads, then the weights' copies, then this thread's output's scale and bias
-  Mx4Block<kXBF16, kGate, kScaled, true> in[kC];
-  auto col0 = [&](int i) __attribute__((always_inline)) { return (wave + W * i) * kRowBlock; };
-#pragma unroll
-  for (int i = 0; i < kC; ++i)
-    in[i].load(t, reinterpret_cast<const char*>(t.x), reinterpret_cast<const char*>(t.gate), col0(i));
+  Mx4Block<kXBF16, kGate, kScaled, true> in;
+  const int col0 = wave * kRowBlock;
+  in.load(t, reinterpret_cast<const char*>(t.x), reinterpret_cast<const char*>(t.gate), col0);
   // (Loads and copies are counted below: in this order.)
   __builtin_amdgcn_sched_barrier(0);
   const uint8_t* const wbase = p.w + n0 * p.ldw;
@@ -69,8 +66,6 @@ __global__ __launch_bounds__(64 * W) void mx4_token_kernel(Mx4Rows t, Mx4Gemm p)
   };
   copy_step(0, stage0);
   if constexpr (S > 1) copy_step(1, stage1);
-  if constexpr (S > 2) copy_step(2, stage2);
-  if constexpr (S > 3) copy_step(3, stage3);
   // (Loads return in order: before the row, these, from memory, would hold it up.
   // Two loads in every thread, of any bytes where there are none, so that all count alike.)
   const int64_t n = n0 + threadIdx.x;
@@ -87,15 +82,13 @@ __global__ __launch_bounds__(64 * W) void mx4_token_kernel(Mx4Rows t, Mx4Gemm p)
   __builtin_amdgcn_s_waitcnt((kVmRow & 15) | ((kVmRow >> 4) << 14) | (7 << 4) | (15 << 8));
   asm volatile("s_nop 0");
   __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    if (col0(i) >= W * S * 512) continue;          // (S == 1: half of the wavefronts have no values)
+  if (col0 < W * S * 512) {                        // (S == 1: half of the wavefronts have no values)
     float v[2][8];
-    in[i].values(t, col0(i), v);
+    in.values(t, col0, v);
     mx4_transform(t, v);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int col = col0(i) + 512 * j;
+      const int col = col0 + 512 * j;
       uint32_t byte;
       const uint32_t w = mx4_piece(v[j], byte);
       reinterpret_cast<uint32_t*>(codes)[col / 8 + lane] = w;
@@ -145,9 +138,6 @@ __global__ __launch_bounds__(64 * W) void mx4_token_kernel(Mx4Rows t, Mx4Gemm p)
   };
   do_step(std::integral_constant<int, 0>{}, stage0);
   if constexpr (S > 1) do_step(std::integral_constant<int, 1>{}, stage1);
-  if constexpr (S > 2) do_step(std::integral_constant<int, 2>{}, stage2);
-  if constexpr (S > 3) do_step(std::integral_constant<int, 3>{}, stage3);
-  static_assert(S <= 4, "steps");
   // (here, by all lanes: the compiler moved the products, and the masks of their
   // scales with them, behind the test below)
   asm volatile("" : "+v"(acc));
@@ -165,12 +155,35 @@ __global__ __launch_bounds__(64 * W) void mx4_token_kernel(Mx4Rows t, Mx4Gemm p)
 
 }  // namespace
 
-// One token, a row of at most 16384 values, 8 at a time, and of more than 8192
-// only where every 16 rows have a compute unit: LDS holds no more of those, and the row would be
-// made again for each (14336 -> 4096 with a gate 10.9 us, in two launches 11.1).
-bool mx4_token_fits(int64_t B, int64_t N, int64_t K, int cus) {
-  if (B != 1 || K % 8 != 0 || N > (int64_t(1) << 26)) return false;
-  return K <= 8192 || (K <= 16384 && (N + 15) / 16 <= (cus > 0 ? cus : 256));
+// One token, a row of at most 16384 values, 8 at a time.
+//
+// Every 16 outputs make the row again, which a second launch would save. What that
+// costs depends on T, the gate and how many workgroups share a compute unit (8 of 4
+// wavefronts with one step each, 4 of those with two, 2 of 8). In us for 16 outputs on every
+// compute unit, weights from memory: the product of two launches takes kPanel + kValue K, with rows
+// of no whole cache lines kRagged more; one launch at most as long without T and gate,
+// and with them at least kMake. The second launch itself costs kSaved. Fitted to 1152
+// measurements; of them the faster way takes 5120 -> 28672 with T 20.7 us in two launches (22.6 in
+// one), 8192 -> 28672 with T 26.2 in one (32.4), 1024 -> 131072 with T and a gate 27.0 in
+// two (32.1), with T 20.1 in one (25.7). profiles/mx4_token_times.txt has others; of those
+// the rule's choice is 0.2% above the faster way on average, and 15% at most.
+//
+// Rows of more than 8192 (16 wavefronts, one workgroup to a unit) where every 16 outputs
+// have a unit: 11264 -> 4096 with T 8.5 us in one launch, 9.7 in two; -> 8192 15.0 and 14.0. From
+// 14336 on without T and gate for any number (16384 -> 28672 44.8 and 54.0), and with both T and a
+// gate not below that (12288 -> 1024 9.5 and 9.0).
+bool mx4_token_fits(int64_t B, int64_t N, int64_t K, int cus, bool transform, bool gate) {
+  if (B != 1 || K % 8 != 0 || K > 16384 || N > (int64_t(1) << 26)) return false;
+  const int64_t panels = (N + 15) / 16;
+  if (cus <= 0) cus = 256;
+  if (K > 8192) return panels <= cus ? K >= 14336 || !(transform && gate) : K >= 14336 && !transform && !gate;
+  if (!transform && !gate) return true;
+  constexpr float kPanel = 0.38f, kValue = 0.394f / 1024.0f, kRagged = 0.12f, kSaved = 2.75f;
+  // T, a gate, both
+  constexpr float kMake[3][3] = {{0.67f, 0.68f, 1.08f}, {0.90f, 0.77f, 1.78f}, {2.95f, 2.83f, 3.58f}};
+  const float make = kMake[K > 4096 ? 2 : K > 2048][!transform ? 1 : gate ? 2 : 0];
+  const float product = (kPanel + kValue * (float)K) * (K % 256 != 0 ? 1.0f + kRagged : 1.0f);
+  return (float)panels / (float)cus * (make - product) <= kSaved;
 }
 
 template <bool kXBF16, bool kGate, bool kScaled>
@@ -179,7 +192,7 @@ static void enqueue_token(const Mx4Rows& t, const Mx4Gemm& p, hipStream_t stream
   if (t.K <= 2048) hipLaunchKernelGGL((mx4_token_kernel<kXBF16, kGate, kScaled, 4, 1>), grid, dim3(256), 0, stream, t, p);
   else if (t.K <= 4096) hipLaunchKernelGGL((mx4_token_kernel<kXBF16, kGate, kScaled, 4, 2>), grid, dim3(256), 0, stream, t, p);
   else if (t.K <= 8192) hipLaunchKernelGGL((mx4_token_kernel<kXBF16, kGate, kScaled, 8, 2>), grid, dim3(512), 0, stream, t, p);
-  else hipLaunchKernelGGL((mx4_token_kernel<kXBF16, kGate, kScaled, 8, 4>), grid, dim3(512), 0, stream, t, p);
+  else hipLaunchKernelGGL((mx4_token_kernel<kXBF16, kGate, kScaled, 16, 2>), grid, dim3(1024), 0, stream, t, p);
 }
 template <bool kXBF16, bool kGate>
 static void enqueue_token(const Mx4Rows& t, const Mx4Gemm& p, hipStream_t stream) {
