@@ -439,8 +439,9 @@ void enqueue_tile(const Mx4Gemm& p, const Mx4Plan& plan, float* partial, hipStre
 // 64 to 28672 inputs; some of them in profiles/mx4_product_times.txt): a step
 // takes `step` plus `share` for every workgroup on the compute unit, a
 // workgroup's begin and end take `ends`, and the weights' stream comes on top at
-// its kernel's rate; rows that are no whole cache lines long take kRagged more. Of
-// these sizes the choice is on average 1.0% above the best of these tiles and splits.
+// its kernel's rate; rows that are no whole cache lines long take kRagged more. With the
+// time of its own choice measured at every size, that is 1.2% above the best of these tiles
+// and splits on average and 17% at most at 317 of those sizes, 1.6% and 17% at 150 others.
 // Left out, with what their absence costs on average: 128 x 256 tokens (0%),
 // 64 x 128 (0.1%), 128 x 64 in 3 steps of 256 bytes (0.1%), 64 x 64 in 2 (0%).
 struct TileCost {
@@ -474,6 +475,10 @@ Mx4Plan plan_mx4(int64_t B, int64_t N, int64_t K, int cus) {
   const float ragged = bytes % 128 != 0 ? 1.0f + kRagged : 1.0f;
   for (const TileCost& c : kTiles) {
     if (c.few && (B > c.tokens || (c.tokens > 4 && B <= c.tokens / 2))) continue;   // (no more codes than needed)
+    // (Wide tiles of mostly no tokens lie outside of what the costs were fitted to, which put them too
+    // low: 24 tokens 512 -> 65536 9.6 us, in 32-token tiles 9.4; 8 tokens 1024 -> 65536 13.5 and 12.5; one
+    // token 11008 -> 65536 in 64-token tiles 70.7, in 32-token ones 67.2.)
+    if (c.tokens >= 128 ? c.tokens >= 4 * B : c.tokens >= 64 * B) continue;
     const uint32_t tiles_n = ((uint32_t)N + c.rows - 1) / c.rows, tiles_b = ((uint32_t)B + c.tokens - 1) / c.tokens;
     if ((uint64_t)tiles_n * tiles_b > (uint64_t)kMaxTiles && &c != kTiles) continue;
     const uint32_t tiles = tiles_n * tiles_b, slots = ucus * c.per_cu, steps = (bytes + c.bytes - 1) / c.bytes;
