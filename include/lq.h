@@ -547,12 +547,13 @@ lq_status lq_norm_block(const lq_norm_block_args* args, void* stream);
  *                                            shorter; blocks begin at k = 0)
  *     e = floor(log2 m) - 2, at least -127  scale byte e + 127
  *     q_k = v_k 2^-e rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and
- *           their negatives (codes 0..7, plus 8 for a negative), ties to the
+ *           their negatives (codes 0..7, plus 8 where v has a minus sign, a
+ *           zero's too), ties to the
  *           even code, magnitudes above 6 to 6
  *     y[n] = row_scale[n] * sum_blocks 2^(e_w + e_q) sum_k w[n][k] q[k]
  *            (+ bias[n])
  *
- * A block of zeros has scale byte 0 and codes 0, a block that holds an
+ * A block of zeros has scale byte 0 (and codes 0 or 8), a block that holds an
  * infinity or a NaN has scale byte 255 (NaN) and codes 0, so the outputs of
  * its row (or, of a weight, of its column) are NaN. Products are summed in
  * fp32, in a fixed order.
