@@ -16,16 +16,17 @@
 //
 // Sums are the instruction's own, fp32, over 128 values and then in order.
 //
-// 2048 tokens 8192 -> 28672 230 us (4.18 PFLOP/s), 28672 -> 8192 192 (5.0), of which
-// the matrix cores are busy for 57%, LDS (operands read twice over, copies
+// 2048 tokens 8192 -> 28672 230 to 239 us (4.0 to 4.2 PFLOP/s), 28672 -> 8192 192 to 202
+// (4.8 to 5.0), of which the matrix cores are busy for 57%, LDS (operands read twice over, copies
 // written) for about half. Copies without products take 179 us, products and reads
 // without copies 127; codes of nothing but zeros, which cost less power, 12% less.
 // One wavefront on a SIMD issues all of it in turn: what gave the copies more time
-// was slower (stages of 64 bytes, four of them, 192 -> 210; copies issued half a step
+// was slower (stages of 64 bytes, four of them, 201 -> 218; copies issued half a step
 // earlier, with a second barrier, 204 -> 232), and so were smaller tiles, which copy
 // more for a product (20480 -> 8192 174 us; in 128 x 128, two to a compute unit, 191,
 // in four stages 223). Larger ones than 256 x 256 have no registers for their sums.
-// 64 tokens 5120 -> 27648 15.3 us, its 75 MB of weights at 4.9 TB/s.
+// 64 tokens 5120 -> 27648 22 us with its 75 MB of weights from memory (3.4 TB/s), 15.4 where
+// the last-level cache holds them.
 #include <type_traits>
 
 #include "lq_mx4_mma.h"

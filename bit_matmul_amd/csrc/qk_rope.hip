@@ -11,9 +11,9 @@
 // first groups are on their way. fp64 there, because position times frequency
 // needs more than fp32 holds from a few thousand positions on.
 //
-// Bound by the bytes for many tokens: 2048 of 64 + 8 heads of 128, bf16, normed and
-// rotated 16.0 us (4.7 TB/s of its 75 MB), rotated alone 14.4, fp32 25.6 (5.9, part of
-// it from caches); 777 of 40 + 8 heads of 80, fp32, 10.5. One token 3.3 us: the launch,
+// Bound by the bytes for many tokens: 2048 of 64 + 8 heads of 128, bf16, from memory,
+// normed and rotated 17.2 us (4.4 TB/s of its 75 MB), rotated alone 15.2, fp32 29.2 (5.2);
+// 777 of 40 + 8 heads of 80, fp32, 10.2. One token 3.0 us, with norms 3.6: the launch,
 // a trip to memory and the angles. A workgroup to a token, whose wavefronts share
 // the angles and so meet once, took 21.4 us where these took 17.6 in their first form.
 #include "lq_qk.h"
