@@ -9,24 +9,25 @@
 
 namespace lq {
 
-// Undoes what fwht_block's exchanges of lane and register bits did to the
+// Undoes what fwht_stages' exchanges of lane and register bits did to the
 // places of values: afterwards v is in the order of its columns again.
+template <int kLaneBit>
+__device__ __forceinline__ void swap_back(float& a, float& b) {
+  uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  lane_swap<kLaneBit>(x, y);
+  a = __uint_as_float(x);
+  b = __uint_as_float(y);
+}
 __device__ __forceinline__ void fwht_restore(float (&v)[2][8], int lhb) {
-  auto swap = [&](auto bit, float& a, float& b) __attribute__((always_inline)) {
-    uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
-    lane_swap<decltype(bit)::value>(x, y);
-    a = __uint_as_float(x);
-    b = __uint_as_float(y);
-  };
   if (lhb > 8) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) swap(std::integral_constant<int, 32>{}, v[0][k], v[1][k]);
+    for (int k = 0; k < 8; ++k) swap_back<32>(v[0][k], v[1][k]);
   }
   if (lhb > 7) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) swap(std::integral_constant<int, 16>{}, v[j][k], v[j][k + 4]);
+      for (int k = 0; k < 4; ++k) swap_back<16>(v[j][k], v[j][k + 4]);
   }
 }
 
@@ -119,21 +120,36 @@ struct Mx4Block {
 // T: of the factor 1 / sqrt(hb) the power of two 2^-ceil(log2(hb) / 2) goes into the
 // values, exactly, so that sums pass the largest float only where (nearly) a result does,
 // and the sqrt(2) that an odd log2 hb leaves multiplies the results, one rounding of each.
-// (1 / sqrt(128) itself in front rounded every one of 128 inputs.)
+// (1 / sqrt(128) itself in front rounded every one of 128 inputs.) The stages go from
+// neighbours to the farthest values, whatever hb, so that v is what the header says to the bit.
 __device__ __forceinline__ void mx4_transform(const Mx4Rows& p, float (&v)[2][8]) {
   if (p.lhb == 0) return;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[j][k] *= p.norm;
-  fwht_block(v, p.lhb);
+  if (p.lhb == 10) {
+    // (bit 9, the pieces', behind bit 8: in the registers that bit 8 used and gives back.
+    // In front of bit 3, where it costs nothing, 2048 x 28672 took 43 us, so 45.)
+    fwht_stages(v, 9);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      swap_back<32>(v[0][k], v[1][k]);
+      const float x = v[0][k], y = v[1][k];
+      v[0][k] = x + y;
+      v[1][k] = x - y;
+    }
+    fwht_restore(v, 8);
+    return;
+  }
+  fwht_stages(v, p.lhb);
+  fwht_restore(v, p.lhb);
   if (p.lhb & 1) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[j][k] *= 1.41421356237309504880f;
   }
-  fwht_restore(v, p.lhb);
 }
 
 }  // namespace lq

@@ -9,7 +9,7 @@
 // ties to the even code, what is above 6 to 6.
 //
 // Bound by the bytes, from memory: 2048 x 28672 bf16 32 us (4.7 TB/s), with a gate 58 (4.5);
-// with T 2048 x 8192 15.4 us, where the same without T takes 10.5: the butterflies and the
+// with T 2048 x 8192 15.7 us, where the same without T takes 10.5: the butterflies and the
 // channel scales, read for every row. 16 rows to a workgroup, whose scales lie together,
 // were no faster, nor was a cheaper sigmoid.
 #include "lq_mx4_rows.h"

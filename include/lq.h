@@ -585,8 +585,8 @@ lq_status lq_mx4_scale_size(int64_t rows, int64_t K, size_t* bytes);
  * 4-bit rows q and their scales of T (act(gate) .* x). Arguments as in
  * lq_quant_rows; q: B rows, ldq bytes apart, whose 16 ceil(K / 32) bytes are
  * written (codes past K as 0); scale: lq_mx4_scale_size(B, K) bytes. v is computed
- * in fp32 (with T the sums, in log2 hb stages, of act(gate) x c 2^-ceil(log2(hb) / 2),
- * times sqrt(2) where log2 hb is odd; a block where one of them passes the
+ * in fp32 (with T the sums, in log2 hb stages from neighbours to values hb / 2 apart, of
+ * act(gate) x c 2^-ceil(log2(hb) / 2), times sqrt(2) where log2 hb is odd; a block where one of them passes the
  * largest float counts as one that holds an infinity); scale and codes are
  * exactly those of that v. Errors: INVALID_ARG and UNSUPPORTED as lq_quant_rows, for
  * K > LQ_MX4_MAX_K, and ldq below 16 ceil(K / 32).
