@@ -173,7 +173,8 @@ __global__ __launch_bounds__(64 * W) void mx4_token_kernel(Mx4Rows t, Mx4Gemm p)
 // 14336 on without T and gate for any number (16384 -> 28672 44.8 and 54.0), and with both T and a
 // gate not below that (12288 -> 1024 9.5 and 9.0).
 bool mx4_token_fits(int64_t B, int64_t N, int64_t K, int cus, bool transform, bool gate) {
-  if (B != 1 || K % 8 != 0 || K > 16384 || N > (int64_t(1) << 26)) return false;
+  // (a launch has fewer than 2^32 threads: 1024 to a workgroup above 8192 inputs)
+  if (B != 1 || K % 8 != 0 || K > 16384 || N > (int64_t(1) << (K > 8192 ? 25 : 26))) return false;
   const int64_t panels = (N + 15) / 16;
   if (cus <= 0) cus = 256;
   if (K > 8192) return panels <= cus ? K >= 14336 || !(transform && gate) : K >= 14336 && !transform && !gate;

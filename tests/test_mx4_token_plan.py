@@ -49,6 +49,14 @@ def test_the_rule_depends_on_what_is_made_again():
     assert fits(8192, 28672, True, False) and not fits(5120, 28672, True, False)
 
 
+@pytest.mark.parametrize("K", [8, 2048, 4096, 8192, 8200, 14336, 16384])
+def test_one_launch_has_fewer_than_2_32_threads(K):
+    waves = 4 if K <= 4096 else 8 if K <= 8192 else 16
+    for log in range(1, 29):
+        for N in ((1 << log) - 1, 1 << log, (1 << log) + 1):
+            assert not fits(K, N, False, False) or -(-N // 16) * 64 * waves < 1 << 32
+
+
 @pytest.mark.parametrize("K,N", [(512, 131072), (5120, 10240), (5120, 28672), (2560, 57344), (8192, 1 << 24), (12288, 4096)])
 def test_the_workspace_holds_two_launches(K, N):
     """Without a gate one launch, with one two: the workspace is asked for before that is known."""
